@@ -21,7 +21,8 @@
  *  - All data pointers are DEVICE pointers owned by the caller. The library
  *    never allocates, frees or synchronizes; every call only enqueues
  *    kernels on `stream` (0 = the null stream) and returns.
- *  - bf16 inputs are row-major with a dense row pitch.
+ *  - bf16 inputs are row-major with a dense row pitch (the norm and int8
+ *    entry points at the end take pitches).
  *  - Packed MXFP4 operand ("nibbles + E8M0 bytes"): nibble byte j of a row
  *    holds element 2j in bits 0-3 and element 2j+1 in bits 4-7; an element
  *    code is sign << 3 | magnitude code (magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6
@@ -54,10 +55,10 @@ typedef enum {
   MXFP4_ERR_NULL = 1,      /* a required pointer is NULL                       */
   MXFP4_ERR_SHAPE = 2,     /* a size is negative, zero where not allowed, or not
                               a multiple of the block / Hadamard size           */
-  MXFP4_ERR_MODE = 3,      /* axis, hadamard, scale_mode or out_dtype invalid  */
-  MXFP4_ERR_WORKSPACE = 4, /* ws_bytes below mxfp4_workspace_bytes()           */
+  MXFP4_ERR_MODE = 3,      /* axis, hadamard, scale_mode or a type invalid     */
+  MXFP4_ERR_WORKSPACE = 4, /* ws_bytes below the call's workspace size         */
   MXFP4_ERR_HIP = 5,       /* the HIP runtime reported an error on launch      */
-  MXFP4_ERR_ALIGN = 6      /* a vector-accessed pointer is not 16-byte aligned */
+  MXFP4_ERR_ALIGN = 6      /* a pointer is not aligned as its entry point says */
 } mxfp4_status;
 
 typedef enum {
@@ -73,6 +74,9 @@ typedef enum {
 } mxfp4_scale_mode;
 
 typedef enum { MXFP4_OUT_F32 = 0, MXFP4_OUT_BF16 = 1 } mxfp4_out;
+
+/* Types of the norm and 8-bit entry points (mxfp4_rmsnorm and below). */
+typedef enum { MXFP4_DT_F32 = 0, MXFP4_DT_BF16 = 1, MXFP4_DT_F16 = 2 } mxfp4_dtype;
 
 typedef enum { MXFP4_OP_FPROP = 0, MXFP4_OP_DGRAD = 1, MXFP4_OP_WGRAD = 2 } mxfp4_op;
 
@@ -344,6 +348,90 @@ int mxfp4_wgrad(const void* dY, const void* X, int64_t T, int64_t N, int64_t K,
 /* Workspace bytes of a fused product (op: mxfp4_op): both packed operands,
  * each piece rounded up to 256 bytes. Returns 0 for invalid arguments. */
 size_t mxfp4_workspace_bytes(int op, int64_t T, int64_t N, int64_t K);
+
+/*
+ * ------------------------------------------------------------------------
+ * RMS norm, int8 operands and the int8 product. They serve the layers around
+ * the MXFP4 products: the norm in front of a linear layer (with its gradient,
+ * in training), and linear layers held in 8 bits.
+ *
+ * Conventions beside those at the top of this file: `dtype` (and out_dtype)
+ * is an mxfp4_dtype; matrices are row-major with a row pitch `ld` in
+ * elements, ld >= cols (any pitch and any alignment to the element's size is
+ * accepted; 16-byte aligned rows whose width is a multiple of 16 bytes are
+ * read 16 bytes at a time). The outputs' memory must not overlap the inputs',
+ * except that h may be x or residual itself. rows == 0 (M or N == 0) is a
+ * valid empty call. All results are deterministic.
+ *
+ * mxfp4_rmsnorm -- for every row: h = x + residual rounded to `dtype` (h = x
+ * where residual is NULL); r = 1 / sqrt(mean(h^2) + eps), the mean in fp64;
+ * y = (h r) weight in fp32, rounded to `dtype` once. weight [cols] is of
+ * `dtype` or fp32 (weight_dtype), NULL for 1. h (the new residual stream) and
+ * rstd ([rows], the r of every row, which mxfp4_rmsnorm_bwd reads) may be
+ * NULL. 1 <= cols <= 32768. eps >= 0; an all-zero row with eps = 0 gives NaN.
+ */
+int mxfp4_rmsnorm(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld,
+                  const void* weight, int weight_dtype, int64_t rows, int64_t cols, float eps,
+                  int dtype, void* h, int64_t h_ld, void* y, int64_t y_ld, float* rstd,
+                  hipStream_t stream);
+
+/*
+ * mxfp4_rmsnorm_int8 -- mxfp4_rmsnorm with y as an int8 operand, quantized
+ * from its fp32 value: with a = max |y| of the row, scales[row] = a / 127 and
+ * codes = rint(y (127 / a)) (ties to even, within +-127), in fp32. A row of
+ * zeros has scale 0 and codes 0; a row that holds a NaN or an infinity has
+ * scale NaN and codes 0. codes [rows][codes_ld] int8, codes_ld >= cols; codes
+ * from cols up to the next multiple of 128 (or to codes_ld, if that is less)
+ * are set to 0, so that a product may run over them.
+ */
+int mxfp4_rmsnorm_int8(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld,
+                       const void* weight, int weight_dtype, int64_t rows, int64_t cols,
+                       float eps, int dtype, void* h, int64_t h_ld, void* codes,
+                       int64_t codes_ld, float* scales, hipStream_t stream);
+
+/*
+ * mxfp4_rmsnorm_bwd -- gradients of mxfp4_rmsnorm. dy: gradient of y; dh:
+ * gradient that reaches h from elsewhere (NULL: none); h and rstd as the
+ * forward pass wrote them (h = x without a residual). With g = dy weight and
+ * u = h rstd: dx = rstd (g - u mean(g u)) + dh, which is the gradient of x
+ * and of residual alike, in `dtype`; dweight [cols] = sum over rows of dy u,
+ * in weight_dtype (NULL: not wanted; with rows == 0 it is set to 0). Sums in
+ * fp32, in a fixed order. ws: mxfp4_rmsnorm_bwd_workspace_bytes(rows, cols)
+ * bytes, 4-byte aligned (NULL where dweight is).
+ */
+int mxfp4_rmsnorm_bwd(const void* dy, int64_t dy_ld, const void* dh, int64_t dh_ld, const void* h,
+                      int64_t h_ld, const void* weight, int weight_dtype, const float* rstd,
+                      int64_t rows, int64_t cols, int dtype, void* dx, int64_t dx_ld,
+                      void* dweight, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t mxfp4_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * mxfp4_int8_quantize -- codes and scales of the rows of x, as
+ * mxfp4_rmsnorm_int8 makes them of y. With `gate` (same shape and type, NULL:
+ * none) of silu(gate) x instead, the gated activation of a feed-forward
+ * block, in fp32 (relative error of silu below 2^-19 + |gate| 2^-23).
+ */
+int mxfp4_int8_quantize(const void* x, int64_t x_ld, const void* gate, int64_t gate_ld,
+                        int64_t rows, int64_t cols, int dtype, void* codes, int64_t codes_ld,
+                        float* scales, hipStream_t stream);
+
+/*
+ * mxfp4_int8_gemm -- C[m][n] = (sum_k A[m][k] B[n][k]) a_scales[m]
+ * b_scales[n] + bias[n]. A [M][lda] and B [N][ldb] int8 codes (any of -128 ..
+ * 127), a_scales [M], b_scales [N] and bias [N] (NULL: none) fp32, C [M][ldc]
+ * of out_dtype, overwritten. The sum is exact (int32; 1 <= K <= 131071) and
+ * rounded once to fp32, as is each of the two products with a scale and the
+ * sum with the bias. A scale of NaN makes its row or column NaN. Operands that are
+ * 16-byte aligned with pitches that are multiples of 16, and K % 128 == 0
+ * (what the quantizers' zero codes allow for any width), take the fast
+ * kernels. ws: mxfp4_int8_gemm_workspace_bytes(M, N, K) bytes, 16-byte
+ * aligned (may be 0, then ws may be NULL).
+ */
+int mxfp4_int8_gemm(const void* A, int64_t lda, const float* a_scales, const void* B, int64_t ldb,
+                    const float* b_scales, const float* bias, int64_t M, int64_t N, int64_t K,
+                    void* C, int64_t ldc, int out_dtype, void* ws, size_t ws_bytes,
+                    hipStream_t stream);
+size_t mxfp4_int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Static text of a status code ("MXFP4_OK", ...); never NULL. */
 const char* mxfp4_status_string(int status);

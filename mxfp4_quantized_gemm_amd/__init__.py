@@ -19,6 +19,7 @@ AXIS_ROW, AXIS_COL, AXIS_2D32 = 0, 1, 2
 SCALE_OCP_FLOOR, SCALE_CEIL = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 OP_FPROP, OP_DGRAD, OP_WGRAD = 0, 1, 2
+DT_F32, DT_BF16, DT_F16 = 0, 1, 2
 ERROR_STATS_COUNT = 10
 ERROR_STATS_WS_BYTES = 1024 * ERROR_STATS_COUNT * 8
 ERROR_STATS_FIELDS = ("sum_e_scale2", "sum_e_dz2", "sum_e_grid2", "dot_scale_grid",
@@ -32,6 +33,8 @@ EXPORTS = (
     "mxfp4_quantize_rs", "mxfp4_quantize_sr", "mxfp4_error_stats",
     "mxfp4_error_stats_noalloc", "mxfp4_gemm", "mxfp4_gemm_mbs", "mxfp4_fprop", "mxfp4_dgrad", "mxfp4_wgrad",
     "mxfp4_workspace_bytes", "mxfp4_status_string",
+    "mxfp4_rmsnorm", "mxfp4_rmsnorm_int8", "mxfp4_rmsnorm_bwd", "mxfp4_rmsnorm_bwd_workspace_bytes",
+    "mxfp4_int8_quantize", "mxfp4_int8_gemm", "mxfp4_int8_gemm_workspace_bytes",
 )
 
 _LIB = None
@@ -81,6 +84,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.restype = i32
     lib.mxfp4_workspace_bytes.argtypes = [i32, i64, i64, i64]
     lib.mxfp4_workspace_bytes.restype = sz
+    f32 = ctypes.c_float
+    lib.mxfp4_rmsnorm.argtypes = [p, i64, p, i64, p, i32, i64, i64, f32, i32, p, i64, p, i64, p, p]
+    lib.mxfp4_rmsnorm.restype = i32
+    lib.mxfp4_rmsnorm_int8.argtypes = lib.mxfp4_rmsnorm.argtypes
+    lib.mxfp4_rmsnorm_int8.restype = i32
+    lib.mxfp4_rmsnorm_bwd.argtypes = [p, i64, p, i64, p, i64, p, i32, p, i64, i64, i32, p, i64, p, p, sz, p]
+    lib.mxfp4_rmsnorm_bwd.restype = i32
+    lib.mxfp4_rmsnorm_bwd_workspace_bytes.argtypes = [i64, i64]
+    lib.mxfp4_rmsnorm_bwd_workspace_bytes.restype = sz
+    lib.mxfp4_int8_quantize.argtypes = [p, i64, p, i64, i64, i64, i32, p, i64, p, p]
+    lib.mxfp4_int8_quantize.restype = i32
+    lib.mxfp4_int8_gemm.argtypes = [p, i64, p, p, i64, p, p, i64, i64, i64, p, i64, i32, p, sz, p]
+    lib.mxfp4_int8_gemm.restype = i32
+    lib.mxfp4_int8_gemm_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.mxfp4_int8_gemm_workspace_bytes.restype = sz
     lib.mxfp4_status_string.argtypes = [i32]
     lib.mxfp4_status_string.restype = ctypes.c_char_p
     _LIB = lib
@@ -452,3 +470,152 @@ def linear(op, P, Q, hadamard=16, scale_mode=SCALE_OCP_FLOOR, out_dtype=OUT_F32,
                       device=P.device)
     fn(P, Q, T, N, K, hadamard, scale_mode, ws, out, out_dtype, stream)
     return out
+
+
+# ------------------------------------------- norm and 8-bit C calls
+# These take 2-D tensors with a unit column stride (any row pitch) and read
+# the sizes, pitches and types off them. They are called once per layer and
+# token in serving, where the host's time counts, so the checks are few and
+# the addresses go to ctypes as plain integers.
+_DT = None
+
+
+def _dt(dtype):
+    global _DT
+    if _DT is None:
+        import torch
+        _DT = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+    try:
+        return _DT[dtype]
+    except KeyError:
+        raise TypeError(f"type must be float32, bfloat16 or float16, got {dtype}") from None
+
+
+def _mat(t, rows, cols, dtype, name):
+    """Address and row pitch of a [rows][cols] matrix on the GPU."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live in GPU memory")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+        raise ValueError(f"{name} must be [{rows}][{cols}], got {list(t.shape)}")
+    s0, s1 = t.stride()
+    if (s1 != 1 and cols > 1) or (s0 < cols and rows > 1):
+        raise ValueError(f"{name} must have a unit column stride and rows that do not overlap")
+    return t.data_ptr(), max(s0, cols)
+
+
+def _vec(t, n, dtype, name):
+    """Address of a vector of at least n values (None: 0)."""
+    if t is None:
+        return 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live in GPU memory")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous values")
+    return t.data_ptr()
+
+
+def _run(fn, args, device, stream):
+    """Call fn(*args, stream) with `device` current; its current stream where None."""
+    import torch
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        raise MXFP4Error(status, fn.__name__)
+
+
+def _norm_args(x, residual, weight, eps, h):
+    dtype = x.dtype
+    rows, cols = x.shape
+    xp, xl = _mat(x, rows, cols, dtype, "x")
+    rp, rl = (0, cols) if residual is None else _mat(residual, rows, cols, dtype, "residual")
+    hp, hl = (0, cols) if h is None else _mat(h, rows, cols, dtype, "h")
+    wt, wp = dtype, 0
+    if weight is not None:
+        wt = weight.dtype
+        if weight.numel() != cols:
+            raise ValueError(f"weight must hold {cols} values, holds {weight.numel()}")
+        wp = _vec(weight, cols, wt, "weight")
+    return (xp, xl, rp, rl, wp, _dt(wt), rows, cols, eps, _dt(dtype), hp, hl), rows, cols
+
+
+def mxfp4_rmsnorm(x, residual, weight, eps, h, y, rstd, stream=None):
+    """RMS norm of ``h = x + residual`` into ``y`` (residual, weight, h and rstd may be None)."""
+    args, rows, cols = _norm_args(x, residual, weight, eps, h)
+    import torch
+    _run(load_library().mxfp4_rmsnorm,
+         (*args, *_mat(y, rows, cols, x.dtype, "y"), _vec(rstd, rows, torch.float32, "rstd")),
+         x.device, stream)
+
+
+def mxfp4_rmsnorm_int8(x, residual, weight, eps, h, codes, scales, stream=None):
+    """The same with int8 codes [rows][>= cols] and scales [rows] in place of ``y``."""
+    import torch
+    args, rows, cols = _norm_args(x, residual, weight, eps, h)
+    _run(load_library().mxfp4_rmsnorm_int8,
+         (*args, *_codes(codes, rows, cols), _vec(scales, rows, torch.float32, "scales")),
+         x.device, stream)
+
+
+def _codes(t, rows, cols):
+    import torch
+    if t.dim() != 2 or t.size(1) < cols:
+        raise ValueError(f"codes must be [{rows}][{cols} or more], got {list(t.shape)}")
+    return _mat(t, rows, t.size(1), torch.int8, "codes")
+
+
+def mxfp4_rmsnorm_bwd(dy, dh, h, weight, rstd, dx, dweight, ws, stream=None):
+    """Gradients of mxfp4_rmsnorm (dh, weight, dweight and ws may be None)."""
+    import torch
+    rows, cols = h.shape
+    dtype = h.dtype
+    wt = dtype if weight is None and dweight is None else (dweight if weight is None else weight).dtype
+    args = (*_mat(dy, rows, cols, dtype, "dy"),
+            *((0, cols) if dh is None else _mat(dh, rows, cols, dtype, "dh")),
+            *_mat(h, rows, cols, dtype, "h"), _vec(weight, cols, wt, "weight"), _dt(wt),
+            _vec(rstd, rows, torch.float32, "rstd"), rows, cols, _dt(dtype),
+            *_mat(dx, rows, cols, dtype, "dx"), _vec(dweight, cols, wt, "dweight"),
+            _vec(ws, 0, torch.uint8, "ws"), 0 if ws is None else ws.numel())
+    _run(load_library().mxfp4_rmsnorm_bwd, args, h.device, stream)
+
+
+def mxfp4_rmsnorm_bwd_workspace_bytes(rows, cols):
+    return int(load_library().mxfp4_rmsnorm_bwd_workspace_bytes(rows, cols))
+
+
+def mxfp4_int8_quantize(x, gate, codes, scales, stream=None):
+    """Int8 codes [rows][>= cols] and scales [rows] of ``x``, or of ``silu(gate) * x``."""
+    import torch
+    rows, cols = x.shape
+    args = (*_mat(x, rows, cols, x.dtype, "x"),
+            *((0, cols) if gate is None else _mat(gate, rows, cols, x.dtype, "gate")),
+            rows, cols, _dt(x.dtype), *_codes(codes, rows, cols),
+            _vec(scales, rows, torch.float32, "scales"))
+    _run(load_library().mxfp4_int8_quantize, args, x.device, stream)
+
+
+def mxfp4_int8_gemm(A, a_scales, B, b_scales, bias, C, ws, stream=None):
+    """C = (A B^T) a_scales b_scales + bias of int8 operands (bias and ws may be None)."""
+    import torch
+    M, K = A.shape
+    N = B.size(0)
+    f32 = torch.float32
+    args = (*_mat(A, M, K, torch.int8, "A"), _vec(a_scales, M, f32, "a_scales"),
+            *_mat(B, N, K, torch.int8, "B"), _vec(b_scales, N, f32, "b_scales"),
+            _vec(bias, N, f32, "bias"), M, N, K, *_mat(C, M, N, C.dtype, "C"), _dt(C.dtype),
+            0 if ws is None else _vec(ws, 0, torch.uint8, "ws"), 0 if ws is None else ws.numel())
+    _run(load_library().mxfp4_int8_gemm, args, A.device, stream)
+
+
+def mxfp4_int8_gemm_workspace_bytes(M, N, K):
+    return int(load_library().mxfp4_int8_gemm_workspace_bytes(M, N, K))

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp4.so")
-SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "stats.hip"]
+SOURCES = ["api.cpp", "api_int8.cpp", "quant.hip", "gemm.hip", "stats.hip", "norm.hip",
+           "int8_gemm.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,536 @@
+// RMS norm with the residual's addition, its gradient, and the int8 row
+// quantizers for gfx950 (MI355X).
+//
+//   h = round_T(x + res)                   the residual stream, held in its type T
+//   r = 1 / sqrt(mean(h^2) + eps)          one factor a row
+//   y = (h r) w
+//   codes: a = max |v| of the row's values v (y; x; or silu(gate) x),
+//          scale = a / 127, q = rint(v (127 / a)); a = 0: scale 0, codes 0;
+//          a row that holds a NaN or an infinity: scale NaN, codes 0
+//   gradient of (y, h): with g = dy w and u = h r,
+//          dx = dres = r (g - u mean(g u)) + dh,  dw = sum over rows of dy u
+//
+// Each is one pass over HBM: a row's values stay in registers between its
+// sums and its output. Precision: products and factors in fp32; the sum of
+// squares in fp64, because h^2 leaves fp32's range for |h| above 2^64, and so
+// that r is the same fp32 number whatever the order of the sum (but for a row
+// in about 10^8 whose factor lies within 2^-50 of a rounding border); the int8
+// codes can then be checked bit for bit against a plain implementation.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "norm_int8.h"
+
+namespace mx {
+namespace {
+
+constexpr int kF32 = 0, kBF16 = 1, kF16 = 2;
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+template <int T>
+struct Type;  // bytes of a value
+template <>
+struct Type<kF32> {
+  static constexpr int S = 4;
+};
+template <>
+struct Type<kBF16> {
+  static constexpr int S = 2;
+};
+template <>
+struct Type<kF16> {
+  static constexpr int S = 2;
+};
+
+// One value of type T at element i of p, as fp32 (exact), and back (RNE).
+template <int T>
+__device__ __forceinline__ float get1(const void* p, int64_t i) {
+  if constexpr (T == kF32) return static_cast<const float*>(p)[i];
+  if constexpr (T == kBF16)
+    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+  if constexpr (T == kF16) return (float)static_cast<const _Float16*>(p)[i];
+}
+
+template <int T>
+__device__ __forceinline__ float round_to(float v) {
+  if constexpr (T == kBF16) return (float)(__bf16)v;
+  if constexpr (T == kF16) return (float)(_Float16)v;
+  return v;
+}
+
+template <int T>
+__device__ __forceinline__ void put1(void* p, int64_t i, float v) {
+  if constexpr (T == kF32) static_cast<float*>(p)[i] = v;
+  if constexpr (T == kBF16) static_cast<__bf16*>(p)[i] = (__bf16)v;
+  if constexpr (T == kF16) static_cast<_Float16*>(p)[i] = (_Float16)v;
+}
+
+// 16 bytes of type T <-> V = 16 / size values.
+template <int T, int V>
+__device__ __forceinline__ void unpack(u32x4 q, float (&v)[V]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if constexpr (T == kF32) {
+      v[d] = __uint_as_float(q[d]);
+    } else if constexpr (T == kBF16) {
+      v[2 * d] = __uint_as_float(q[d] << 16);
+      v[2 * d + 1] = __uint_as_float(q[d] & 0xffff0000u);
+    } else {
+      const uint32_t e = q[d];  // a bit_cast of the element itself reads element 0
+      const f16x2 h = __builtin_bit_cast(f16x2, e);
+      v[2 * d] = (float)h.x;
+      v[2 * d + 1] = (float)h.y;
+    }
+  }
+}
+
+template <int T, int V>
+__device__ __forceinline__ u32x4 pack(const float (&v)[V]) {
+  u32x4 q;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if constexpr (T == kF32) {
+      q[d] = __float_as_uint(v[d]);
+    } else if constexpr (T == kBF16) {
+      const bf16x2 h = {(__bf16)v[2 * d], (__bf16)v[2 * d + 1]};
+      q[d] = __builtin_bit_cast(uint32_t, h);
+    } else {
+      const f16x2 h = {(_Float16)v[2 * d], (_Float16)v[2 * d + 1]};
+      q[d] = __builtin_bit_cast(uint32_t, h);
+    }
+  }
+  return q;
+}
+
+// A thread's share of a row: chunk i (i < R) holds the V consecutive values
+// from column (t + TPR i) V on, so that a load covers TPR V consecutive
+// values. V is 16 bytes' worth, or 1 where the row's address, pitch or width
+// does not fit 16 bytes. Columns past the row read as 0 and are not written.
+template <int T, int V, int TPR, int R>
+struct Row {
+  static __device__ __forceinline__ void load(const void* p, int64_t row0, int cols, int t,
+                                              float (&v)[R][V]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (t + TPR * i) * V;
+      if constexpr (V == 1) {
+        v[i][0] = c < cols ? get1<T>(p, row0 + c) : 0.f;
+      } else {
+        u32x4 q = {0, 0, 0, 0};
+        if (c < cols)
+          q = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p) +
+                                              (row0 + c) * Type<T>::S);
+        unpack<T, V>(q, v[i]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t row0, int cols, int t,
+                                               const float (&v)[R][V]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (t + TPR * i) * V;
+      if (c < cols) {
+        if constexpr (V == 1)
+          put1<T>(p, row0 + c, v[i][0]);
+        else
+          *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p) + (row0 + c) * Type<T>::S) =
+              pack<T, V>(v[i]);
+      }
+    }
+  }
+};
+
+// The weight's values of a thread's columns; its type is T or fp32. The
+// vector form needs 16-byte alignment too (the launcher sees to it).
+template <int T, int V, int TPR, int R>
+__device__ __forceinline__ void load_weight(const void* w, bool wide, int cols, int t,
+                                            float (&v)[R][V]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[i][k] = 1.f;
+  } else if (T == kF32 || !wide) {
+    Row<T, V, TPR, R>::load(w, 0, cols, t, v);
+  } else if constexpr (V == 1) {
+    Row<kF32, 1, TPR, R>::load(w, 0, cols, t, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (t + TPR * i) * V;
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const u32x4 q = c < cols ? *reinterpret_cast<const u32x4*>(static_cast<const float*>(w) + c + k)
+                                 : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][k + e] = __uint_as_float(q[e]);
+      }
+    }
+  }
+}
+
+// Sum (or integer max) over the TPR threads of a row; every thread gets it.
+// `red` holds one slot per wave; each call uses slots of its own, so one
+// barrier is enough. The order is fixed.
+template <int TPR, class X, class F>
+__device__ __forceinline__ X reduce_row(X v, X* red, int t, F f) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = f(v, __shfl_xor(v, o));
+  if constexpr (TPR > 64) {
+    if ((t & 63) == 0) red[t >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < TPR / 64; ++w) v = f(v, red[w]);
+  }
+  return v;
+}
+
+__device__ __forceinline__ double add64(double a, double b) { return a + b; }
+__device__ __forceinline__ float add32(float a, float b) { return a + b; }
+__device__ __forceinline__ uint32_t max32(uint32_t a, uint32_t b) { return max(a, b); }
+
+// Codes and scale of a row of values. 127 / a overflows for a below 2^-120,
+// so a row of small values is first scaled by 2^64, which is exact.
+template <int V, int TPR, int R>
+__device__ __forceinline__ void write_codes(const float (&v)[R][V], uint32_t* red, uint8_t* q,
+                                            int64_t ld, float* scale, int cols, int t) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) m = max(m, __float_as_uint(v[i][k]) & 0x7fffffffu);
+  m = reduce_row<TPR>(m, red, t, max32);
+  const bool bad = m >= 0x7f800000u;
+  const float a = __uint_as_float(m);
+  const float up = a < 0x1p-64f ? 0x1p64f : 1.f;
+  const float inv = (bad || m == 0) ? 0.f : 127.f / (a * up);
+  if (t == 0) *scale = bad ? __uint_as_float(0x7fc00000u) : a / 127.f;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int c = (t + TPR * i) * V;
+    if (c >= cols) continue;
+    uint32_t d[(V + 3) / 4] = {};
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int code = bad ? 0 : (int)rintf(v[i][k] * up * inv);
+      d[k / 4] |= ((uint32_t)code & 255u) << (8 * (k & 3));
+    }
+    if constexpr (V == 1)
+      q[c] = (uint8_t)d[0];
+    else if constexpr (V == 4)
+      *reinterpret_cast<uint32_t*>(q + c) = d[0];
+    else
+      *reinterpret_cast<u32x2*>(q + c) = u32x2{d[0], d[1]};
+  }
+  // zero codes up to a multiple of 128 columns, as far as the pitch has them
+  const int end = (int)min((int64_t)(cols + 127) / 128 * 128, ld);
+  for (int c = cols + t; c < end; c += TPR) q[c] = 0;
+}
+
+// silu(g) u = g u / (1 + exp(-g)), by the hardware's base-2 exponential and
+// reciprocal (each within about one ulp; the rounded argument g log2(e) adds
+// at most |g| 2^-24 to the relative error): far below half a step of a code.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);
+  return g * __builtin_amdgcn_rcpf(1.f + e) * u;
+}
+
+constexpr int kNorm = 0, kNormInt8 = 1, kQuant = 2, kSwiglu = 3;
+
+struct RowArgs {
+  const void *x, *res, *w;  // res: the residual (norm) or the gate (swiglu)
+  void *h, *out;
+  float* stat;  // rstd (norm, may be NULL) or scales
+  int64_t x_ld, res_ld, h_ld, out_ld, rows;
+  int cols;
+  float eps;
+  bool wide;  // fp32 weight beside 16-bit inputs
+};
+
+template <int T, int V, int TPR, int R, int OP>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(RowArgs A) {
+  constexpr int NW = TPR < 256 ? 4 : TPR / 64;
+  __shared__ double red64[NW];
+  __shared__ uint32_t red32[NW];
+  // below 256 threads a row, a work-group takes 256 / TPR rows
+  const int t = TPR < 256 ? threadIdx.x % TPR : threadIdx.x;
+  const int64_t group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t row = TPR < 256 ? group * (256 / TPR) + threadIdx.x / TPR : group;
+  if (row >= A.rows) return;  // whole waves up to 64 threads a row, else whole work-groups
+  typedef Row<T, V, TPR, R> X;
+  float v[R][V];
+  X::load(A.x, row * A.x_ld, A.cols, t, v);
+  if constexpr (OP == kSwiglu) {
+    float g[R][V];
+    X::load(A.res, row * A.res_ld, A.cols, t, g);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[i][k] = swiglu(g[i][k], v[i][k]);
+  }
+  if constexpr (OP == kNorm || OP == kNormInt8) {
+    if (A.res != nullptr) {
+      float b[R][V];
+      X::load(A.res, row * A.res_ld, A.cols, t, b);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][k] = round_to<T>(v[i][k] + b[i][k]);
+    }
+    if (A.h != nullptr) X::store(A.h, row * A.h_ld, A.cols, t, v);
+    float w[R][V];
+    load_weight<T, V, TPR, R>(A.w, A.wide, A.cols, t, w);
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) s = fma((double)v[i][k], (double)v[i][k], s);
+    s = reduce_row<TPR>(s, red64, t, add64);
+    const float r = (float)(1.0 / sqrt(s / (double)A.cols + (double)A.eps));
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[i][k] = v[i][k] * r * w[i][k];
+    if constexpr (OP == kNorm) {
+      if (A.stat != nullptr && t == 0) A.stat[row] = r;
+      X::store(A.out, row * A.out_ld, A.cols, t, v);
+    }
+  }
+  if constexpr (OP != kNorm)
+    write_codes<V, TPR, R>(v, red32, static_cast<uint8_t*>(A.out) + row * A.out_ld, A.out_ld,
+                           A.stat + row, A.cols, t);
+}
+
+// ------------------------------------------------------------- gradient
+struct BwdArgs {
+  const void *dy, *dh, *h, *w;
+  const float* rstd;
+  void* dx;
+  float* part;  // [gridDim.x][cols] partial sums of dw, or NULL
+  int64_t dy_ld, dh_ld, h_ld, dx_ld, rows;
+  int cols;
+  bool wide;
+};
+
+// Work-groups walk rows blockIdx.x, + gridDim.x, ...: the weight's gradient
+// is summed over a work-group's rows in registers, and the work-groups'
+// partial sums by a second kernel in a fixed order (no atomics).
+template <int T, int V, int TPR, int R>
+__global__ __launch_bounds__(TPR) void bwd_kernel(BwdArgs A) {
+  __shared__ float red[2][TPR / 64];
+  const int t = threadIdx.x;
+  typedef Row<T, V, TPR, R> X;
+  float w[R][V], dw[R][V];
+  load_weight<T, V, TPR, R>(A.w, A.wide, A.cols, t, w);
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) dw[i][k] = 0.f;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
+    float g[R][V], u[R][V];
+    X::load(A.dy, row * A.dy_ld, A.cols, t, g);
+    X::load(A.h, row * A.h_ld, A.cols, t, u);
+    const float r = A.rstd[row];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        u[i][k] *= r;
+        dw[i][k] = fmaf(g[i][k], u[i][k], dw[i][k]);
+        g[i][k] *= w[i][k];
+        s = fmaf(g[i][k], u[i][k], s);
+      }
+    float d[R][V];
+    if (A.dh != nullptr) {
+      X::load(A.dh, row * A.dh_ld, A.cols, t, d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) d[i][k] = 0.f;
+    }
+    // two sets of slots: a row's slots are written again two rows later,
+    // after the barrier of the row between
+    s = reduce_row<TPR>(s, red[turn], t, add32) / (float)A.cols;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) d[i][k] = fmaf(r, g[i][k] - u[i][k] * s, d[i][k]);
+    X::store(A.dx, row * A.dx_ld, A.cols, t, d);
+  }
+  if (A.part != nullptr) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = (t + TPR * i) * V + k;
+        if (c < A.cols) A.part[(int64_t)blockIdx.x * A.cols + c] = dw[i][k];
+      }
+  }
+}
+
+// dw[c] = sum over the parts p of part[p][c]: 16 waves of a work-group take
+// every 16th part of 64 columns, then their sums meet in order.
+template <int T>
+__global__ __launch_bounds__(1024) void dw_kernel(const float* part, int parts, int cols, void* dw) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int p = wave; p < parts; p += 16) s += part[(int64_t)p * cols + c];
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += red[k][lane];
+    put1<T>(dw, c, s);
+  }
+}
+
+bool fits(const void* p, int64_t ld, int vec, int bytes) {
+  return p == nullptr || ((uintptr_t)p % (size_t)(vec * bytes) == 0 && ld % vec == 0);
+}
+
+// A grid dimension holds below 2^32 threads: many rows go into two dimensions.
+constexpr int64_t kGridX = int64_t(1) << 20;
+
+template <int T, int V, int TPR, int E, int OP>
+hipError_t go(const RowArgs& A, hipStream_t st) {
+  constexpr int per = TPR < 256 ? 256 / TPR : 1;
+  const int64_t groups = (A.rows + per - 1) / per, gx = groups < kGridX ? groups : kGridX;
+  const dim3 grid((unsigned)gx, (unsigned)((groups + gx - 1) / gx)), blk(TPR < 256 ? 256 : TPR);
+  hipLaunchKernelGGL((row_kernel<T, V, TPR, E / V, OP>), grid, blk, 0, st, A);
+  return hipGetLastError();
+}
+
+// Threads a row and values a thread: one wave up to 1024 columns, 4 waves up
+// to 8192, 16 waves up to kRowMax.
+template <int T, int V, int OP>
+hipError_t go_width(const RowArgs& A, hipStream_t st) {
+  if (A.cols <= 512) return go<T, V, 64, 8, OP>(A, st);
+  if (A.cols <= 1024) return go<T, V, 64, 16, OP>(A, st);
+  if (A.cols <= 4096) return go<T, V, 256, 16, OP>(A, st);
+  if (A.cols <= 8192) return go<T, V, 256, 32, OP>(A, st);
+  if (A.cols <= 16384) return go<T, V, 1024, 16, OP>(A, st);
+  return go<T, V, 1024, 32, OP>(A, st);
+}
+
+template <int T, int OP>
+hipError_t go_vec(const RowArgs& A, hipStream_t st) {
+  constexpr int S = Type<T>::S, V = 16 / S;
+  constexpr int OS = OP == kNorm ? S : 1;
+  const bool vec = A.cols % V == 0 && fits(A.x, A.x_ld, V, S) && fits(A.res, A.res_ld, V, S) &&
+                   fits(A.h, A.h_ld, V, S) && fits(A.out, A.out_ld, V, OS) &&
+                   (uintptr_t)A.w % 16 == 0;
+  return vec ? go_width<T, V, OP>(A, st) : go_width<T, 1, OP>(A, st);
+}
+
+template <int OP>
+hipError_t go_type(const RowArgs& A, int dtype, hipStream_t st) {
+  switch (dtype) {
+    case kBF16: return go_vec<kBF16, OP>(A, st);
+    case kF16: return go_vec<kF16, OP>(A, st);
+    default: return go_vec<kF32, OP>(A, st);
+  }
+}
+
+// Work-groups of the gradient: 16 waves a CU (work-groups are of one or two
+// waves up to 1024 columns, of four or more above), few enough that their
+// partial sums stay small beside the rows themselves.
+int64_t bwd_groups(int64_t rows, int64_t cols) {
+  const int64_t most = cols <= 1024 ? 4096 : 1024;
+  return rows < most ? rows : most;
+}
+
+template <int T, int V, int TPR, int E>
+hipError_t go_bwd(const BwdArgs& A, hipStream_t st) {
+  hipLaunchKernelGGL((bwd_kernel<T, V, TPR, E / V>), dim3((unsigned)bwd_groups(A.rows, A.cols)), dim3(TPR),
+                     0, st, A);
+  return hipGetLastError();
+}
+
+template <int T, int V>
+hipError_t go_bwd_width(const BwdArgs& A, hipStream_t st) {
+  if (A.cols <= 512) return go_bwd<T, V, 64, 8>(A, st);
+  if (A.cols <= 1024) return go_bwd<T, V, 128, 8>(A, st);
+  if (A.cols <= 4096) return go_bwd<T, V, 256, 16>(A, st);
+  if (A.cols <= 16384) return go_bwd<T, V, 1024, 16>(A, st);
+  return go_bwd<T, V, 1024, 32>(A, st);
+}
+
+template <int T>
+hipError_t go_bwd_vec(const BwdArgs& A, hipStream_t st) {
+  constexpr int S = Type<T>::S, V = 16 / S;
+  const bool vec = A.cols % V == 0 && fits(A.dy, A.dy_ld, V, S) && fits(A.dh, A.dh_ld, V, S) &&
+                   fits(A.h, A.h_ld, V, S) && fits(A.dx, A.dx_ld, V, S) && (uintptr_t)A.w % 16 == 0;
+  return vec ? go_bwd_width<T, V>(A, st) : go_bwd_width<T, 1>(A, st);
+}
+
+RowArgs row_args(CMat x, CMat res, const void* w, int wdt, int64_t rows, int64_t cols, float eps,
+                 int dtype, Mat h, Mat out, float* stat) {
+  return RowArgs{x.p,   res.p, w,      h.p,  out.p,     stat, x.ld, res.ld,
+                 h.ld, out.ld, rows, (int)cols, eps, w != nullptr && wdt == kF32 && dtype != kF32};
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(CMat x, CMat res, const void* weight, int weight_dtype, int64_t rows,
+                          int64_t cols, float eps, int dtype, Mat h, Mat y, float* rstd,
+                          hipStream_t stream) {
+  return go_type<kNorm>(row_args(x, res, weight, weight_dtype, rows, cols, eps, dtype, h, y, rstd),
+                        dtype, stream);
+}
+
+hipError_t launch_rmsnorm_int8(CMat x, CMat res, const void* weight, int weight_dtype,
+                               int64_t rows, int64_t cols, float eps, int dtype, Mat h, Mat q,
+                               float* scales, hipStream_t stream) {
+  return go_type<kNormInt8>(
+      row_args(x, res, weight, weight_dtype, rows, cols, eps, dtype, h, q, scales), dtype, stream);
+}
+
+hipError_t launch_int8_quantize(CMat x, CMat gate, int64_t rows, int64_t cols, int dtype, Mat q,
+                                float* scales, hipStream_t stream) {
+  const RowArgs A =
+      row_args(x, gate, nullptr, kF32, rows, cols, 0.f, dtype, Mat{nullptr, 0}, q, scales);
+  return gate.p ? go_type<kSwiglu>(A, dtype, stream) : go_type<kQuant>(A, dtype, stream);
+}
+
+size_t rmsnorm_bwd_ws(int64_t rows, int64_t cols) {
+  return (size_t)bwd_groups(rows, cols) * (size_t)cols * sizeof(float);
+}
+
+hipError_t launch_rmsnorm_bwd(CMat dy, CMat dh, CMat h, const void* weight, int weight_dtype,
+                              const float* rstd, int64_t rows, int64_t cols, int dtype, Mat dx,
+                              void* dweight, void* ws, hipStream_t stream) {
+  const BwdArgs A{dy.p,  dh.p,  h.p,  weight, rstd,      dx.p, dweight ? static_cast<float*>(ws) : nullptr,
+                  dy.ld, dh.ld, h.ld, dx.ld,  rows, (int)cols, weight && weight_dtype == kF32 && dtype != kF32};
+  if (rows > 0) {
+    const hipError_t e = dtype == kBF16  ? go_bwd_vec<kBF16>(A, stream)
+                         : dtype == kF16 ? go_bwd_vec<kF16>(A, stream)
+                                         : go_bwd_vec<kF32>(A, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (dweight == nullptr) return hipSuccess;
+  const dim3 grid((unsigned)((cols + 63) / 64)), blk(1024);
+  const int parts = (int)bwd_groups(rows, cols);
+  const float* p = static_cast<const float*>(ws);
+  if (weight_dtype == kBF16)
+    hipLaunchKernelGGL((dw_kernel<kBF16>), grid, blk, 0, stream, p, parts, (int)cols, dweight);
+  else if (weight_dtype == kF16)
+    hipLaunchKernelGGL((dw_kernel<kF16>), grid, blk, 0, stream, p, parts, (int)cols, dweight);
+  else
+    hipLaunchKernelGGL((dw_kernel<kF32>), grid, blk, 0, stream, p, parts, (int)cols, dweight);
+  return hipGetLastError();
+}
+
+}  // namespace mx
