@@ -419,9 +419,10 @@ int mxfp4_int8_quantize(const void* x, int64_t x_ld, const void* gate, int64_t g
  * mxfp4_int8_gemm -- C[m][n] = (sum_k A[m][k] B[n][k]) a_scales[m]
  * b_scales[n] + bias[n]. A [M][lda] and B [N][ldb] int8 codes (any of -128 ..
  * 127), a_scales [M], b_scales [N] and bias [N] (NULL: none) fp32, C [M][ldc]
- * of out_dtype, overwritten. The sum is exact (int32; 1 <= K <= 131071) and
- * rounded once to fp32, as is each of the two products with a scale and the
- * sum with the bias. A scale of NaN makes its row or column NaN. Operands that are
+ * of out_dtype, overwritten. The sum is exact (int32; 1 <= K <= 131071); it,
+ * its product with a_scales[m], and that times b_scales[n] plus the bias
+ * round to fp32 once each, then to out_dtype, so the result does not depend
+ * on the kernel that serves it. A scale of NaN makes its row or column NaN. Operands that are
  * 16-byte aligned with pitches that are multiples of 16, and K % 128 == 0
  * (what the quantizers' zero codes allow for any width), take the fast
  * kernels. ws: mxfp4_int8_gemm_workspace_bytes(M, N, K) bytes, 16-byte

@@ -8,6 +8,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <type_traits>
+
 #include "norm_int8.h"
 
 namespace mx {
@@ -27,9 +30,10 @@ struct Args {
   int64_t lda, ldb, ldc, M, N, K;
 };
 
-// The scaled sum; one rounding in each step.
-__device__ __forceinline__ float scaled(int acc, float sa, float sb) {
-  return (float)acc * sa * sb;
+// The scaled sum: the int32 sum, its product with sa and the whole round to
+// fp32 once each. Every kernel ends in this, so they agree bit for bit.
+__device__ __forceinline__ float scaled(int acc, float sa, float sb, float bias) {
+  return fmaf((float)acc * sa, sb, bias);
 }
 
 template <int OUT>
@@ -37,6 +41,19 @@ __device__ __forceinline__ void put(void* C, int64_t i, float v) {
   if constexpr (OUT == kF32) static_cast<float*>(C)[i] = v;
   if constexpr (OUT == kBF16) static_cast<__bf16*>(C)[i] = (__bf16)v;
   if constexpr (OUT == kF16) static_cast<_Float16*>(C)[i] = (_Float16)v;
+}
+
+template <int OUT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  if constexpr (OUT == kBF16) {
+    const b2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+  } else {
+    const h2 v = {(_Float16)lo, (_Float16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+  }
 }
 
 // ------------------------------------------------------ general kernel
@@ -99,7 +116,7 @@ __global__ __launch_bounds__(256) void gemm_kernel(Args P, bool vec) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int64_t m = m0 + wm * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-    if (m < P.M) put<OUT>(P.C, m * P.ldc + n, scaled(acc[e], P.sa[m], sb) + bias);
+    if (m < P.M) put<OUT>(P.C, m * P.ldc + n, scaled(acc[e], P.sa[m], sb, bias));
   }
 }
 
@@ -113,14 +130,724 @@ hipError_t launch(const Args& P, hipStream_t st) {
 
 }  // namespace gen
 
+// ------------------------------------------------ LDS DMA building blocks
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ rsrc_t make_rsrc(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes,
+                                           0x00020000);
+}
+
+// One LDS DMA instruction: lane l's B bytes (4 or 16) at buffer offset voff +
+// soff land at lds + B l. A lane whose voff lies past the resource's bytes
+// reads zero.
+template <int B>
+__device__ __forceinline__ void dma(rsrc_t r, uint8_t* lds, uint32_t voff, uint32_t soff) {
+  static_assert(B == 4 || B == 16, "dwords or four of them");
+  if constexpr (B == 4)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, voff, soff, 0, 0);
+  else
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, 0);
+}
+
+// s_waitcnt with vmcnt (and lgkmcnt 0 where LG) constrained.
+template <int N, bool LG = false>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | ((LG ? 0 : 15) << 8));
+}
+
+// Rows of an operand from row r0 on, at most n of them, as a buffer.
+__device__ __forceinline__ rsrc_t rows_rsrc(const uint8_t* p, int64_t r0, int64_t rows, int64_t n,
+                                            int64_t ld) {
+  return make_rsrc(p + r0 * ld, min(rows - r0, n) * ld);
+}
+
+// k-tiles are 128 bytes of every operand row, row-major in LDS, 16-byte chunk
+// c of row r at slot c ^ ((r >> 1) & 7): a DMA instruction (8 whole rows) stays
+// contiguous, 8 lanes fetch a whole 128-byte row, and the 16 lanes of a
+// fragment read (one chunk of rows r .. r + 15) land on distinct banks.
+constexpr int KB = 128;
+
+// Offset of lane l's chunk in DMA block u (rows 8 u .. 8 u + 7).
+__device__ __forceinline__ uint32_t dma_off(int u, int lane, int64_t ld) {
+  const int row = 8 * u + (lane >> 3);
+  return (uint32_t)(row * ld + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
+}
+
+// LDS offset of the fragment of k-step s: chunk 2 s + lane / 32 of row lane % 32.
+__device__ __forceinline__ uint32_t frag_off(int s, int lane) {
+  const int l32 = lane & 31, h = lane >> 5;
+  return (uint32_t)(l32 * KB + (((2 * s + h) ^ ((l32 >> 1) & 7)) << 4));
+}
+
+// Work-group id -> output tile. Consecutive ids go round-robin over the 8
+// XCDs; each XCD gets a contiguous range of logical tiles, walked in groups
+// of 4 tile-rows, so that the tiles resident on one XCD share operand rows in
+// its L2.
+__device__ __forceinline__ void tile_of(int64_t wg, int64_t nwg, int64_t ntm, int64_t ntn,
+                                        int64_t& tm, int64_t& tn) {
+  const int64_t per = nwg / 8;
+  int64_t lg = wg;
+  if (wg < per * 8) lg = (wg % 8) * per + wg / 8;
+  const int64_t width = 4 * ntn, g = lg / width, first = g * 4;
+  const int64_t gs = min(ntm - first, (int64_t)4), r = lg % width;
+  tm = first + r % gs;
+  tn = r / gs;
+}
+
+// ------------------------------------------------------- few tokens (M <= 16 MG)
+// The weight's bytes are the work. A work-group owns 16 rows of B and its W
+// waves split k: chunk c of 64 bytes of the 16 rows belongs to wave c % W,
+// loaded straight into registers in the MFMA's layout (lane l: row l % 16, 16
+// bytes at 16 (l / 16)), so W waves read 64 W consecutive bytes of each row.
+// A wave keeps U chunks in flight: a chunk's registers are loaded again right
+// after its MFMA. Chunks past the end are loads out of the buffer's range
+// (zero, no traffic), so that a round of U has no branches. The tokens (A) come
+// from the caches. Partial sums meet in LDS.
+namespace few {
+
+template <int W, int U, int MG, int OUT>
+__global__ __launch_bounds__(64 * W) void gemm_kernel(Args P) {
+  __shared__ int red[W][MG][64 * 4];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const rsrc_t rb = rows_rsrc(P.B, n0, P.N, 16, P.ldb), ra = rows_rsrc(P.A, 0, P.M, 16 * MG, P.lda);
+  const uint32_t vb = (uint32_t)((lane & 15) * P.ldb + 16 * (lane >> 4));
+  uint32_t va[MG];
+#pragma unroll
+  for (int g = 0; g < MG; ++g) va[g] = (uint32_t)((16 * g + (lane & 15)) * P.lda + 16 * (lane >> 4));
+  const int chunks = (int)(P.K / 64);
+  v4i acc[MG], qb[U], qa[U][MG];
+#pragma unroll
+  for (int g = 0; g < MG; ++g) acc[g] = v4i{0, 0, 0, 0};
+  auto load = [&](int u, int c) {
+    const uint32_t dead = c < chunks ? 0u : 0x80000000u;  // rows are below 2^23 bytes
+    const uint32_t so = (uint32_t)c * 64;
+    qb[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, vb | dead, so, 2));
+#pragma unroll
+    for (int g = 0; g < MG; ++g)
+      qa[u][g] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, va[g] | dead, so, 0));
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, wave + W * u);
+  auto mul = [&](int u) {
+#pragma unroll
+    for (int g = 0; g < MG; ++g)
+      acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(qb[u], qa[u][g], acc[g], 0, 0, 0);
+  };
+  for (int c = W * U; c < chunks; c += W * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mul(u);
+      load(u, c + wave + W * u);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) mul(u);
+  // register e of lane l is row 4 (l / 16) + e of B, token l % 16
+#pragma unroll
+  for (int g = 0; g < MG; ++g) *reinterpret_cast<v4i*>(&red[wave][g][4 * lane]) = acc[g];
+  __syncthreads();
+  for (int i = t; i < 256 * MG; i += 64 * W) {
+    const int g = i >> 8, m = (i >> 4) & 15, n = i & 15;
+    const int64_t row = 16 * g + m, col = n0 + n;
+    if (row >= P.M || col >= P.N) continue;
+    int s = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += red[w][g][4 * (m + 16 * (n >> 2)) + (n & 3)];
+    put<OUT>(P.C, row * P.ldc + col, scaled(s, P.sa[row], P.sb[col], P.bias ? P.bias[col] : 0.f));
+  }
+}
+
+template <int W, int U, int MG, int OUT>
+hipError_t launch(const Args& P, hipStream_t st) {
+  hipLaunchKernelGGL((gemm_kernel<W, U, MG, OUT>), dim3((unsigned)((P.N + 15) / 16)), dim3(64 * W), 0, st,
+                     P);
+  return hipGetLastError();
+}
+
+}  // namespace few
+
+// ------------------------------------------- ring of k-tiles (middle sizes)
+// WM x WN waves of TM x TN MFMA tiles; k-tiles run through a ring of NS LDS
+// buffers filled by DMA NS - 1 ahead, one barrier a k-tile. Where there
+// are fewer output tiles than CUs the k range is split over blockIdx.y: the
+// int32 partial sums go to the workspace and a second kernel adds them (the
+// sums are exact, so the split does not show in the result).
+namespace ring {
+
+template <int WM_, int WN_, int TM_, int TN_, int NS_, int SP_ = 4>
+struct G {
+  static constexpr int SP = SP_;  // k-steps that a k-tile's DMAs are spread over
+  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NS = NS_;
+  static constexpr int NW = WM * WN, NT = 64 * NW;
+  static constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
+  static constexpr int NB = (BM + BN) / 8 / NW;  // DMA blocks (8 rows) per wave and k-tile
+  static constexpr int STAGE = (BM + BN) * KB;
+  static_assert((BM + BN) % (8 * NW) == 0, "DMA blocks divide over the waves");
+  static_assert(NS >= 2 && NS <= 4 && (NS - 1) * NB < 64, "vmcnt range");
+};
+
+template <class T>
+struct Frag {
+  v4i a[T::TM], b[T::TN];
+};
+
+template <class T>
+struct Lane {
+  uint32_t off[T::NB];  // DMA offsets
+  uint32_t fa[4], fb[4];
+};
+
+// DMAs [U0, U1) of the k-tile at byte ko into st; nothing is fetched where it is not live.
+template <class T, int U0 = 0, int U1 = T::NB>
+__device__ __forceinline__ void fetch(uint8_t* st, rsrc_t ra, rsrc_t rb, rsrc_t none, bool live,
+                                      const Lane<T>& L, uint32_t ko, int wave) {
+#pragma unroll
+  for (int u = U0; u < U1; ++u) {
+    const int blk = T::NW * u + wave;  // uniform: blocks of A, then of B
+    dma<16>(!live ? none : 8 * blk < T::BM ? ra : rb, st + blk * 1024, L.off[u], ko);
+  }
+}
+
+template <class T, int S>
+__device__ __forceinline__ void read(const uint8_t* st, const Lane<T>& L, Frag<T>& F) {
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i) F.a[i] = *reinterpret_cast<const v4i*>(st + L.fa[S] + i * 32 * KB);
+#pragma unroll
+  for (int j = 0; j < T::TN; ++j) F.b[j] = *reinterpret_cast<const v4i*>(st + L.fb[S] + j * 32 * KB);
+}
+
+template <class T>
+__device__ __forceinline__ void mul(const Frag<T>& F, v16i (&acc)[T::TM][T::TN]) {
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F.a[i], F.b[j], acc[i][j], 0, 0, 0);
+}
+
+// Scheduling of a k-step: its LDS reads and DMAs spread over its MFMAs (left
+// alone, the compiler bunches them behind the MFMAs). DMAs come after an MFMA:
+// a wave waits at a DMA while the load unit is busy, and an MFMA then runs.
+template <class T, int R, int NL>
+__device__ __forceinline__ void interleave() {
+  constexpr int NM = T::TM * T::TN, NR = T::TM + T::TN;
+  if constexpr (R < NM) {
+    constexpr int r = NR * (R + 1) / NM - NR * R / NM, l = NL * (R + 1) / NM - NL * R / NM;
+    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(0x020, l, 0);
+    interleave<T, R + 1, NL>();
+  } else {
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <class T, int OUT>
+__global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* part) {
+  constexpr int NS = T::NS, NB = T::NB;
+  __shared__ __attribute__((aligned(16))) uint8_t s0[T::STAGE], s1[T::STAGE], s2[NS > 2 ? T::STAGE : 16],
+      s3[NS > 3 ? T::STAGE : 16];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  const int64_t ntm = (P.M + T::BM - 1) / T::BM, ntn = (P.N + T::BN - 1) / T::BN;
+  int64_t tm, tn;
+  tile_of(blockIdx.x, gridDim.x, ntm, ntn, tm, tn);
+  const int64_t m0 = tm * T::BM, n0 = tn * T::BN;
+  // the split's k-tiles: [k0, k0 + nk), at least one
+  const int all = (int)(P.K / KB), z = blockIdx.y;
+  const int k0 = (int)((int64_t)all * z / splits), nk = (int)((int64_t)all * (z + 1) / splits) - k0;
+  const rsrc_t ra = rows_rsrc(P.A, m0, P.M, T::BM, P.lda), rb = rows_rsrc(P.B, n0, P.N, T::BN, P.ldb);
+  const rsrc_t none = make_rsrc(P.A, 0);
+  Lane<T> L;
+#pragma unroll
+  for (int u = 0; u < NB; ++u) {
+    const int blk = T::NW * u + wave;
+    L.off[u] = 8 * blk < T::BM ? dma_off(blk, lane, P.lda) : dma_off(blk - T::BM / 8, lane, P.ldb);
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    L.fa[s] = (uint32_t)(wm * T::TM * 32 * KB) + frag_off(s, lane);
+    L.fb[s] = (uint32_t)((T::BM + wn * T::TN * 32) * KB) + frag_off(s, lane);
+  }
+  v16i acc[T::TM][T::TN];
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) acc[i][j] = v16i{};
+
+  auto slot = [&](int s) { return s == 0 ? s0 : s == 1 ? s1 : s == 2 ? s2 : s3; };
+  // the first NS - 1 k-tiles and the first part of the next; the first k-tile
+  // has landed when only the others' DMAs are outstanding
+#pragma unroll
+  for (int k = 0; k < NS - 1; ++k)
+    fetch<T>(slot(k), ra, rb, none, k < nk, L, (uint32_t)(k0 + k) * KB, wave);
+  fetch<T, 0, NB / T::SP>(slot(NS - 1), ra, rb, none, NS - 1 < nk, L, (uint32_t)(k0 + NS - 1) * KB, wave);
+  wait_vm<(NS - 2) * NB + NB / T::SP>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frag<T> F0, F1;
+  read<T, 0>(s0, L, F0);
+  // k-tile k in slot S: a k-step's MFMAs run on fragments read during the
+  // k-step before. The barrier before the last k-step publishes k-tile k + 1
+  // (each wave's own DMAs of it have landed, the later ones stay in flight)
+  // and retires slot S (each wave's reads of it are done), which takes k-tile
+  // k + NS: the first of its SP parts here, the others with the first k-steps
+  // of k-tile k + 1.
+  auto part_of = [&](auto S, auto Q, int k) {  // part Q of k-tile k into slot S
+    constexpr int u0 = NB * Q.value / T::SP, u1 = NB * (Q.value + 1) / T::SP;
+    if constexpr (Q.value < T::SP)
+      fetch<T, u0, u1>(slot(S.value), ra, rb, none, k < nk, L, (uint32_t)(k0 + k) * KB, wave);
+  };
+  auto count = [](int q) { return q < T::SP ? NB * (q + 1) / T::SP - NB * q / T::SP : 0; };
+  auto step = [&](auto S, int k) {
+    constexpr std::integral_constant<int, (S.value + NS - 1) % NS> before{};
+    uint8_t* st = slot(S.value);
+    read<T, 1>(st, L, F1);
+    mul<T>(F0, acc);
+    part_of(before, std::integral_constant<int, 1>{}, k - 1 + NS);
+    interleave<T, 0, count(1)>();
+    read<T, 2>(st, L, F0);
+    mul<T>(F1, acc);
+    part_of(before, std::integral_constant<int, 2>{}, k - 1 + NS);
+    interleave<T, 0, count(2)>();
+    read<T, 3>(st, L, F1);
+    mul<T>(F0, acc);
+    part_of(before, std::integral_constant<int, 3>{}, k - 1 + NS);
+    interleave<T, 0, count(3)>();
+    wait_vm<(NS - 2) * NB, true>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read<T, 0>(slot((S.value + 1) % NS), L, F0);
+    part_of(S, std::integral_constant<int, 0>{}, k + NS);
+    mul<T>(F1, acc);
+    interleave<T, 0, count(0)>();
+  };
+  // Only a whole turn of the ring reaches the loop's back edge: the compiler
+  // would else see a path on which slot 0 was just fetched, and wait for it.
+  for (int k = 0;; k += NS) {
+    step(std::integral_constant<int, 0>{}, k);
+    if (k + 1 >= nk) break;
+    step(std::integral_constant<int, 1>{}, k + 1);
+    if (k + 2 >= nk) break;
+    if constexpr (NS > 2) {
+      step(std::integral_constant<int, 2>{}, k + 2);
+      if (k + 3 >= nk) break;
+    }
+    if constexpr (NS > 3) {
+      step(std::integral_constant<int, 3>{}, k + 3);
+      if (k + 4 >= nk) break;
+    }
+  }
+  wait_vm<0>();  // the last (empty) DMAs still write LDS: let them land
+
+  const int half = lane >> 5, l32 = lane & 31;
+#pragma unroll
+  for (int j = 0; j < T::TN; ++j) {
+    const int64_t n = n0 + (wn * T::TN + j) * 32 + l32;
+    if (n >= P.N) continue;
+    const bool whole = splits == 1;
+    const float sb = whole ? P.sb[n] : 0.f, bias = whole && P.bias ? P.bias[n] : 0.f;
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t m = m0 + (wm * T::TM + i) * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
+        if (m >= P.M) continue;
+        if (whole)
+          put<OUT>(P.C, m * P.ldc + n, scaled(acc[i][j][e], P.sa[m], sb, bias));
+        else
+          part[((int64_t)z * P.M + m) * P.N + n] = acc[i][j][e];
+      }
+  }
+}
+
+template <int OUT>
+__global__ __launch_bounds__(256) void sum_kernel(Args P, int splits, const int* part) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
+  if (n >= P.N) return;
+  int s = 0;
+#pragma unroll 4
+  for (int z = 0; z < splits; ++z) s += part[((int64_t)z * P.M + m) * P.N + n];
+  put<OUT>(P.C, m * P.ldc + n, scaled(s, P.sa[m], P.sb[n], P.bias ? P.bias[n] : 0.f));
+}
+
+template <class T, int OUT>
+hipError_t launch(const Args& P, int splits, void* ws, hipStream_t st) {
+  const int64_t tiles = ((P.M + T::BM - 1) / T::BM) * ((P.N + T::BN - 1) / T::BN);
+  hipLaunchKernelGGL((gemm_kernel<T, OUT>), dim3((unsigned)tiles, splits), dim3(T::NT), 0, st, P, splits,
+                     static_cast<int*>(ws));
+  if (splits > 1) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((sum_kernel<OUT>), dim3((unsigned)((P.N + 255) / 256), (unsigned)P.M), dim3(256), 0,
+                       st, P, splits, static_cast<const int*>(ws));
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ring
+
+// --------------------------------------------------- large products
+// Persistent: one 512-thread work-group per CU walks 256 x 256 output tiles,
+// 8 waves (2 x 4) of 128 x 64, that is 4 x 2 MFMA tiles and 128 accumulators
+// a lane. Two LDS stages of one k-tile each, filled by DMA: a k-tile's four
+// k-steps of 8 MFMAs each run on fragments that were read during the k-step
+// before, the next k-tile's DMAs are issued in two halves one k-step apart,
+// and the barrier comes before the last k-step, whose MFMAs run after it
+// together with the first reads of the next k-tile. The operand stream does
+// not stop at a tile's end: the last k-tiles prefetch the next tile's first.
+// The tile's scales and bias come by DMA too (its first k-tile), so that the
+// epilogue waits for no load.
+namespace big {
+
+constexpr int BM = 256, BN = 256, TM = 4, TN = 2, WN = 4;
+constexpr int TILE = BM * KB, STAGE = 2 * TILE;
+constexpr int DA = 4;  // DMA blocks of an operand per wave and k-tile
+
+struct Tile {
+  rsrc_t a, b;
+  int64_t m0, n0;
+};
+
+struct Frag {
+  v4i a[TM], b[TN];
+};
+
+struct Offs {
+  uint32_t a[DA], b[DA], fa[4], fb[4];
+};
+
+// Half H of k-tile kk into st: of the current tile, of the next one when kk
+// runs past the (even) number of k-tiles np, nothing where there is none.
+template <int H>
+__device__ __forceinline__ void fetch(uint8_t* st, const Tile& c, const Tile& n, bool has_next,
+                                      rsrc_t none, const Offs& O, int kk, int nk, int np, int wave) {
+  const bool nx = kk >= np;
+  const int k = nx ? kk - np : kk;
+  const bool live = k < nk && (!nx || has_next);
+  const rsrc_t ra = live ? (nx ? n.a : c.a) : none, rb = live ? (nx ? n.b : c.b) : none;
+  const uint32_t ko = (uint32_t)k * KB;
+#pragma unroll
+  for (int u = 2 * H; u < 2 * H + 2; ++u) dma<16>(ra, st + (DA * wave + u) * 1024, O.a[u], ko);
+#pragma unroll
+  for (int u = 2 * H; u < 2 * H + 2; ++u) dma<16>(rb, st + TILE + (DA * wave + u) * 1024, O.b[u], ko);
+}
+
+template <int S>
+__device__ __forceinline__ void read(const uint8_t* st, const Offs& O, Frag& F) {
+#pragma unroll
+  for (int i = 0; i < TM; ++i) F.a[i] = *reinterpret_cast<const v4i*>(st + O.fa[S] + i * 32 * KB);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) F.b[j] = *reinterpret_cast<const v4i*>(st + O.fb[S] + j * 32 * KB);
+}
+
+__device__ __forceinline__ void mul(const Frag& F, v16i (&acc)[TN][TM]) {
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F.a[i], F.b[j], acc[j][i], 0, 0, 0);
+}
+
+// One MFMA, then an LDS read and a DMA where there are any left, and so on.
+template <int R, int NR, int NL>
+__device__ __forceinline__ void interleave() {
+  constexpr int NM = TM * TN;
+  if constexpr (R < NM) {
+    constexpr int r = R < NR ? (R == NM - 1 ? NR - R : 1) : 0;
+    constexpr int l = NL * (R + 1) / NM - NL * R / NM;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+    if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(0x020, l, 0);
+    interleave<R + 1, NR, NL>();
+  }
+}
+
+// k-tile k of the current tile, in st; F0 holds its first fragments. The
+// stage nx holds k-tile k + 1 but for its second half.
+__device__ __forceinline__ void ktile(uint8_t* st, uint8_t* nx, const Tile& c, const Tile& n,
+                                      bool has_next, rsrc_t none, const Offs& O, Frag& F0, Frag& F1,
+                                      v16i (&acc)[TN][TM], int k, int nk, int np, int wave) {
+  constexpr int NR = TM + TN;
+  read<1>(st, O, F1);
+  mul(F0, acc);
+  fetch<1>(nx, c, n, has_next, none, O, k + 1, nk, np, wave);
+  interleave<0, NR, 4>();
+  __builtin_amdgcn_sched_barrier(0);
+  read<2>(st, O, F0);
+  mul(F1, acc);
+  interleave<0, NR, 0>();
+  __builtin_amdgcn_sched_barrier(0);
+  read<3>(st, O, F1);
+  mul(F0, acc);
+  interleave<0, NR, 0>();
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vm<0>();
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  read<0>(nx, O, F0);
+  fetch<0>(st, c, n, has_next, none, O, k + 2, nk, np, wave);
+  mul(F1, acc);
+  interleave<0, NR, 4>();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ Tile tile_at(const Args& P, int64_t vt, int64_t ntiles, int64_t ntm,
+                                        int64_t ntn) {
+  Tile T;
+  int64_t tm, tn;
+  tile_of(vt, ntiles, ntm, ntn, tm, tn);
+  T.m0 = tm * BM;
+  T.n0 = tn * BN;
+  T.a = rows_rsrc(P.A, T.m0, P.M, BM, P.lda);
+  T.b = rows_rsrc(P.B, T.n0, P.N, BN, P.ldb);
+  return T;
+}
+
+template <int OUT>
+__global__ __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2)))
+void gemm_kernel(Args P, bool pairs) {
+  __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
+  __shared__ __attribute__((aligned(16))) float sc[2][3 * 256];  // sa, sb, bias of a tile
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int half = lane >> 5, l32 = lane & 31;
+  const int64_t ntm = (P.M + BM - 1) / BM, ntn = (P.N + BN - 1) / BN, ntiles = ntm * ntn;
+  const int64_t step = gridDim.x;
+  const int nk = (int)(P.K / KB), np = (nk + 1) & ~1;
+  const int arow0 = wm * TM * 32, brow0 = wn * TN * 32;
+  const rsrc_t none = make_rsrc(P.A, 0);
+  Offs O;
+#pragma unroll
+  for (int u = 0; u < DA; ++u) {
+    O.a[u] = dma_off(DA * wave + u, lane, P.lda);
+    O.b[u] = dma_off(DA * wave + u, lane, P.ldb);
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    O.fa[s] = (uint32_t)(arow0 * KB) + frag_off(s, lane);
+    O.fb[s] = (uint32_t)(TILE + brow0 * KB) + frag_off(s, lane);
+  }
+  int64_t vt = blockIdx.x;
+  Tile c = tile_at(P, vt, ntiles, ntm, ntn);
+  bool has_next = vt + step < ntiles;
+  Tile n = has_next ? tile_at(P, vt + step, ntiles, ntm, ntn) : c;
+  int turn = 0;
+
+  // k-tile 0 and the first half of k-tile 1; no LDS reads come before this
+  // barrier, so no release fence (it would wait for the later DMAs too)
+  fetch<0>(st0, c, n, has_next, none, O, 0, nk, np, wave);
+  fetch<1>(st0, c, n, has_next, none, O, 0, nk, np, wave);
+  fetch<0>(st1, c, n, has_next, none, O, 1, nk, np, wave);
+  wait_vm<4>();
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  Frag F0, F1;
+  read<0>(st0, O, F0);
+
+  v16i acc[TN][TM];
+  for (;;) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int i = 0; i < TM; ++i) acc[j][i] = v16i{};
+    // waves 0-3: the rows' scales; 4-7: the columns' scales and bias. Read
+    // after the last k-tile, several barriers later; the buffers alternate,
+    // so no wave still reads the one that is filled.
+    {
+      uint8_t* s = reinterpret_cast<uint8_t*>(sc[turn]);
+      const int w = wave & 3;
+      if (wave < 4) {
+        dma<4>(make_rsrc(P.sa + c.m0, min(P.M - c.m0, (int64_t)BM) * 4), s + w * 256,
+               (w * 64 + lane) * 4, 0);
+      } else {
+        const int64_t nb = min(P.N - c.n0, (int64_t)BN) * 4;
+        dma<4>(make_rsrc(P.sb + c.n0, nb), s + 1024 + w * 256, (w * 64 + lane) * 4, 0);
+        dma<4>(P.bias ? make_rsrc(P.bias + c.n0, nb) : none, s + 2048 + w * 256, (w * 64 + lane) * 4, 0);
+      }
+    }
+    for (int k = 0; k < np; k += 2) {
+      ktile(st0, st1, c, n, has_next, none, O, F0, F1, acc, k, nk, np, wave);
+      ktile(st1, st0, c, n, has_next, none, O, F0, F1, acc, k + 1, nk, np, wave);
+    }
+    // acc[j][i] register 4 q + e: row arow0 + 32 i + 8 q + 4 half + e, column
+    // brow0 + 32 j + l32
+    const float* s = sc[turn];
+    float sb[TN], bias[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      sb[j] = s[256 + brow0 + 32 * j + l32];
+      bias[j] = s[512 + brow0 + 32 * j + l32];
+    }
+    const bool full = pairs && c.m0 + BM <= P.M && c.n0 + BN <= P.N;
+    constexpr int EB = OUT == kF32 ? 4 : 2;
+    const rsrc_t rc = make_rsrc(static_cast<uint8_t*>(P.C) + (c.m0 * P.ldc + c.n0) * EB, 256 * P.ldc * EB);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 sa4 = *reinterpret_cast<const float4*>(s + arow0 + 32 * i + 8 * q + 4 * half);
+        const float sa[4] = {sa4.x, sa4.y, sa4.z, sa4.w};
+        float v[TN][4];
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][e] = scaled(acc[j][i][4 * q + e], sa[e], sb[j], bias[j]);
+        if (!full) {
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int64_t m = c.m0 + arow0 + 32 * i + 8 * q + 4 * half + e;
+              const int64_t nn = c.n0 + brow0 + 32 * j + l32;
+              if (m < P.M && nn < P.N) put<OUT>(P.C, m * P.ldc + nn, v[j][e]);
+            }
+        } else if constexpr (OUT == kF32) {
+          // one register: two whole 128-byte row segments
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+              __builtin_amdgcn_raw_buffer_store_b32(
+                  __float_as_uint(v[j][e]), rc,
+                  (uint32_t)((arow0 + 4 * half) * P.ldc + brow0 + 32 * j + l32) * 4,
+                  (uint32_t)((32 * i + 8 * q + e) * P.ldc * 4), 2);
+        } else {
+          // Swapping halves of the two 32-column blocks gives a register 64
+          // consecutive columns of one row; two rows then trade values
+          // between neighbouring lanes: one 4-byte store holds two columns,
+          // even lanes of row R, odd lanes of row R + 1.
+          const int odd = lane & 1;
+          const uint32_t vb = (uint32_t)((arow0 + odd) * P.ldc + brow0 + lane - odd) * 2;
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const auto s0 = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[0][e]),
+                                                             __float_as_uint(v[1][e]), false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(
+                __float_as_uint(v[0][e + 1]), __float_as_uint(v[1][e + 1]), false, false);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // rows 8 q + e + 4 h and the next one
+              const uint32_t x = s0[h], y = s1[h];
+              const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? x : y), 0xb1, 0xf, 0xf, false);
+              const float lo = __uint_as_float(odd ? got : x), hi = __uint_as_float(odd ? y : got);
+              __builtin_amdgcn_raw_buffer_store_b32(
+                  pack2<OUT>(lo, hi), rc, vb, (uint32_t)((32 * i + 8 * q + e + 4 * h) * P.ldc * 2), 2);
+            }
+          }
+        }
+      }
+    if (!has_next) break;
+    vt += step;
+    c = n;
+    has_next = vt + step < ntiles;
+    if (has_next) n = tile_at(P, vt + step, ntiles, ntm, ntn);
+    turn ^= 1;
+  }
+  wait_vm<0>();  // the last (empty) DMAs still write LDS: let them land
+}
+
+// Compute units of the current device, queried once per device.
+int cu_count() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> cache[kMaxDevices];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return 256;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    int c = 0;
+    n = (hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && c > 0) ? c : 256;
+    cache[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <int OUT>
+hipError_t launch(const Args& P, hipStream_t st) {
+  const int64_t tiles = ((P.M + BM - 1) / BM) * ((P.N + BN - 1) / BN), ncu = cu_count();
+  // 4-byte stores of two 16-bit values need even pitches and a 4-byte base
+  const bool pairs = OUT == kF32 || (P.ldc % 2 == 0 && (uintptr_t)P.C % 4 == 0);
+  hipLaunchKernelGGL((gemm_kernel<OUT>), dim3((unsigned)(tiles < ncu ? tiles : ncu)), dim3(512), 0, st, P,
+                     pairs && P.ldc < (int64_t(1) << 22));
+  return hipGetLastError();
+}
+
+}  // namespace big
+
+// The DMA kernels: 16-byte rows, whole k-tiles, 32-bit offsets within a tile.
+bool fast_ok(const Args& P) {
+  return (((uintptr_t)P.A | (uintptr_t)P.B) & 15) == 0 && ((P.lda | P.ldb) & 15) == 0 && P.K % KB == 0 &&
+         P.lda < (int64_t(1) << 23) && P.ldb < (int64_t(1) << 23);
+}
+
+// ----------------------------------------------------------- choice
+// The largest tile that still gives at least kFill tiles, that is work for
+// most of the 256 CUs; measured at K = 4096, N = 6144 (us, 64 x 128 / 128 x
+// 128 / 128 x 256 / 256 x 256 tiles): M = 256 16.7 / 19.7 / 30.0 / 39.9, M =
+// 512 30.9 / 21.3 / 30.4 / 39.9, M = 1024 48.7 / 41.8 / 34.9 / 40.3, M = 2048
+// 95.7 / 70.9 / 68.0 / 47.7. Where even the smallest tile gives fewer, k is
+// split to fill the CUs, with at least kMinTiles k-tiles a split (4096 x 14336
+// weight, M = 128: 42.3 unsplit, 26.2 in two, 21.4 in four).
+typedef ring::G<2, 4, 1, 1, 4, 3> R64x128;
+typedef ring::G<4, 4, 1, 1, 4, 2> R128x128;
+typedef ring::G<4, 4, 1, 2, 3, 3> R128x256;
+
+constexpr int64_t kCUs = 256, kFill = 160, kMinTiles = 4, kMaxSplits = 16;
+enum Kind { kFew, k64x128, k128x128, k128x256, k256x256 };
+
+struct Plan {
+  Kind kind;
+  int splits;
+};
+
+int64_t tiles_of(int64_t M, int64_t N, int64_t bm, int64_t bn) {
+  return ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+}
+
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  // Few tokens: no LDS staging, one launch (M = 4, us against the ring's best:
+  // 4096 x 14336 weight 13.8 / 15.8, 28672 x 4096 24.5 / 28.5, 1024 x 4096 4.9 /
+  // 8.6; at M = 16 18.6 / 15.9, 34.9 / 29.3 and 6.0 / 8.5).
+  if (M <= 8 || (M <= 16 && N * K <= (int64_t(1) << 24))) return {kFew, 1};
+  if (tiles_of(M, N, 256, 256) >= kFill) return {k256x256, 1};
+  if (tiles_of(M, N, 128, 256) >= kFill) return {k128x256, 1};
+  if (tiles_of(M, N, 128, 128) >= kFill) return {k128x128, 1};
+  const int64_t t = tiles_of(M, N, 64, 128), nk = K / KB;
+  int64_t s = t >= kFill ? 1 : kCUs / t;
+  s = s < nk / kMinTiles ? s : nk / kMinTiles;
+  s = s < kMaxSplits ? s : kMaxSplits;
+  return {k64x128, (int)(s > 1 ? s : 1)};
+}
+
 template <int OUT>
 hipError_t launch_out(const Args& P, void* ws, hipStream_t st) {
-  return gen::launch<OUT>(P, st);
+  if (!fast_ok(P)) return gen::launch<OUT>(P, st);
+  const Plan plan = plan_of(P.M, P.N, P.K);
+  switch (plan.kind) {
+    case kFew: return few::launch<8, 4, 1, OUT>(P, st);
+    case k64x128: return ring::launch<R64x128, OUT>(P, plan.splits, ws, st);
+    case k128x128: return ring::launch<R128x128, OUT>(P, 1, ws, st);
+    case k128x256: return ring::launch<R128x256, OUT>(P, 1, ws, st);
+    default: return big::launch<OUT>(P, st);
+  }
 }
 
 }  // namespace
 
-size_t int8_gemm_ws(int64_t M, int64_t N, int64_t K) { return 0; }
+size_t int8_gemm_ws(int64_t M, int64_t N, int64_t K) {
+  if (K % KB) return 0;
+  const int splits = plan_of(M, N, K).splits;
+  return splits > 1 ? (size_t)splits * (size_t)M * (size_t)N * sizeof(int) : 0;
+}
 
 hipError_t launch_int8_gemm(CMat A, const float* sa, CMat B, const float* sb, const float* bias,
                             int64_t M, int64_t N, int64_t K, Mat C, int out_dtype, void* ws,
