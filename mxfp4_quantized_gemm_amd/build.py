@@ -1,9 +1,10 @@
-"""Build libmxfp4.so (gfx950) in-tree with hipcc.
+"""Build libmxfp4.so (gfx950) in-tree with hipcc, and the torch binding of the
+norm and 8-bit operators (_ops.so, host code only) with g++.
 
 Usage: python -m mxfp4_quantized_gemm_amd.build  (or build() from Python).
 Every HIP source is compiled with -ffp-contract=off (the rotation butterfly
 is an exact sequence of fp32 adds) and with packed-fp32 instructions
-disabled. Objects go to _build/, the library next to this file.
+disabled. Objects go to _build/, the libraries next to this file.
 """
 from __future__ import annotations
 
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp4.so")
+OPS = os.path.join(PKG, "_ops.so")
 SOURCES = ["api.cpp", "api_int8.cpp", "quant.hip", "gemm.hip", "stats.hip", "norm.hip",
            "int8_gemm.hip"]
 ARCH = "gfx950"
@@ -52,17 +55,49 @@ def _compile(src: str) -> str:
     return out
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n" + r.stderr)
+
+
+def _compile_ops() -> str:
+    """torch_ops.cpp -> object: host code against torch's and HIP's headers."""
+    import torch
+    from torch.utils import cpp_extension
+    out = os.path.join(BUILD, "torch_ops.cpp.o")
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-c", "-D__HIP_PLATFORM_AMD__",
+          "-DUSE_ROCM", "-DTORCH_EXTENSION_NAME=_ops", "-DTORCH_API_INCLUDE_EXTENSION_H",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(f for d in [*cpp_extension.include_paths(), os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
+                        sysconfig.get_paths()["include"]] for f in ("-isystem", d)),
+          os.path.join(CSRC, "torch_ops.cpp"), "-o", out], "g++ on torch_ops.cpp")
+    return out
+
+
+def _link_ops(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run([shutil.which("g++") or "g++", "-shared", "-o", OPS + ".tmp", obj, "-L" + PKG, "-l:libmxfp4.so",
+          "-L" + libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs], "linking _ops.so")
+    os.replace(OPS + ".tmp", OPS)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libmxfp4.so; returns the library path."""
+    """Compile every source and link both libraries; returns libmxfp4.so's path."""
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ops = ex.submit(_compile_ops)
         objs = list(ex.map(_compile, SOURCES))
+        ops = ops.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stderr)
     os.replace(tmp, LIB)
+    _link_ops(ops)
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -157,6 +157,8 @@ def test_wrappers_refuse_cpu_tensors_and_wrong_shapes():
         norm.rms_norm(x, w, residual=x[:2])
     with pytest.raises(ValueError, match="one dimension"):
         norm.rms_norm(x, x)
+    with pytest.raises(ValueError, match="dimension"):
+        norm.rms_norm(x[0, 0])
     with pytest.raises(ValueError, match="GPU memory"):
         int8.int8_quantize(x)
     with pytest.raises(ValueError, match="gate"):
@@ -167,4 +169,4 @@ def test_wrappers_refuse_cpu_tensors_and_wrong_shapes():
     with pytest.raises(ValueError, match="last dimension"):
         int8.Int8Linear(32, 16)(x)
     with pytest.raises(ValueError, match="columns"):
-        int8._product(q, s, 100, torch.zeros(8, 64, dtype=torch.int8), s, None, torch.bfloat16)
+        int8.int8_linear(x, torch.zeros(8, 100, dtype=torch.int8), s)
