@@ -142,11 +142,13 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* p, int64_t bytes) {
 // One LDS DMA instruction: lane l's B bytes (4 or 16) at buffer offset voff +
 // soff land at lds + B l. A lane whose voff lies past the resource's bytes
 // reads zero.
-template <int B>
+template <int B, int NT = 0>
 __device__ __forceinline__ void dma(rsrc_t r, uint8_t* lds, uint32_t voff, uint32_t soff) {
   static_assert(B == 4 || B == 16, "dwords or four of them");
   if constexpr (B == 4)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, voff, soff, 0, 0);
+  else if constexpr (NT)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, 2);
   else
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, voff, soff, 0, 0);
 }
@@ -208,25 +210,30 @@ __device__ __forceinline__ void tile_of(int64_t wg, int64_t nwg, int64_t ntm, in
 // from the caches. Partial sums meet in LDS.
 namespace few {
 
-template <int W, int U, int MG, int OUT>
+template <int W, int U, int MG, int NG, int OUT>
 __global__ __launch_bounds__(64 * W) void gemm_kernel(Args P) {
-  __shared__ int red[W][MG][64 * 4];
+  __shared__ int red[W][MG * NG][64 * 4];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const rsrc_t rb = rows_rsrc(P.B, n0, P.N, 16, P.ldb), ra = rows_rsrc(P.A, 0, P.M, 16 * MG, P.lda);
-  const uint32_t vb = (uint32_t)((lane & 15) * P.ldb + 16 * (lane >> 4));
-  uint32_t va[MG];
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NG);
+  const rsrc_t rb = rows_rsrc(P.B, n0, P.N, 16 * NG, P.ldb), ra = rows_rsrc(P.A, 0, P.M, 16 * MG, P.lda);
+  uint32_t va[MG], vb[NG];
 #pragma unroll
   for (int g = 0; g < MG; ++g) va[g] = (uint32_t)((16 * g + (lane & 15)) * P.lda + 16 * (lane >> 4));
-  const int chunks = (int)(P.K / 64);
-  v4i acc[MG], qb[U], qa[U][MG];
 #pragma unroll
-  for (int g = 0; g < MG; ++g) acc[g] = v4i{0, 0, 0, 0};
+  for (int h = 0; h < NG; ++h) vb[h] = (uint32_t)((16 * h + (lane & 15)) * P.ldb + 16 * (lane >> 4));
+  const int chunks = (int)(P.K / 64);
+  v4i acc[NG][MG], qb[U][NG], qa[U][MG];
+#pragma unroll
+  for (int h = 0; h < NG; ++h)
+#pragma unroll
+    for (int g = 0; g < MG; ++g) acc[h][g] = v4i{0, 0, 0, 0};
   auto load = [&](int u, int c) {
     const uint32_t dead = c < chunks ? 0u : 0x80000000u;  // rows are below 2^23 bytes
     const uint32_t so = (uint32_t)c * 64;
-    qb[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, vb | dead, so, 2));
+#pragma unroll
+    for (int h = 0; h < NG; ++h)
+      qb[u][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, vb[h] | dead, so, 2));
 #pragma unroll
     for (int g = 0; g < MG; ++g)
       qa[u][g] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, va[g] | dead, so, 0));
@@ -235,8 +242,10 @@ __global__ __launch_bounds__(64 * W) void gemm_kernel(Args P) {
   for (int u = 0; u < U; ++u) load(u, wave + W * u);
   auto mul = [&](int u) {
 #pragma unroll
-    for (int g = 0; g < MG; ++g)
-      acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(qb[u], qa[u][g], acc[g], 0, 0, 0);
+    for (int h = 0; h < NG; ++h)
+#pragma unroll
+      for (int g = 0; g < MG; ++g)
+        acc[h][g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(qb[u][h], qa[u][g], acc[h][g], 0, 0, 0);
   };
   for (int c = W * U; c < chunks; c += W * U) {
 #pragma unroll
@@ -249,23 +258,26 @@ __global__ __launch_bounds__(64 * W) void gemm_kernel(Args P) {
   for (int u = 0; u < U; ++u) mul(u);
   // register e of lane l is row 4 (l / 16) + e of B, token l % 16
 #pragma unroll
-  for (int g = 0; g < MG; ++g) *reinterpret_cast<v4i*>(&red[wave][g][4 * lane]) = acc[g];
+  for (int h = 0; h < NG; ++h)
+#pragma unroll
+    for (int g = 0; g < MG; ++g) *reinterpret_cast<v4i*>(&red[wave][h * MG + g][4 * lane]) = acc[h][g];
   __syncthreads();
-  for (int i = t; i < 256 * MG; i += 64 * W) {
-    const int g = i >> 8, m = (i >> 4) & 15, n = i & 15;
-    const int64_t row = 16 * g + m, col = n0 + n;
+  for (int i = t; i < 256 * MG * NG; i += 64 * W) {
+    const int n = i % (16 * NG), m = i / (16 * NG);  // neighbouring threads, neighbouring columns
+    const int64_t row = m, col = n0 + n;
     if (row >= P.M || col >= P.N) continue;
+    const int at = (n >> 4) * MG + (m >> 4), l = 4 * ((m & 15) + 16 * ((n & 15) >> 2)) + (n & 3);
     int s = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) s += red[w][g][4 * (m + 16 * (n >> 2)) + (n & 3)];
+    for (int w = 0; w < W; ++w) s += red[w][at][l];
     put<OUT>(P.C, row * P.ldc + col, scaled(s, P.sa[row], P.sb[col], P.bias ? P.bias[col] : 0.f));
   }
 }
 
-template <int W, int U, int MG, int OUT>
+template <int W, int U, int MG, int NG, int OUT>
 hipError_t launch(const Args& P, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_kernel<W, U, MG, OUT>), dim3((unsigned)((P.N + 15) / 16)), dim3(64 * W), 0, st,
-                     P);
+  hipLaunchKernelGGL((gemm_kernel<W, U, MG, NG, OUT>), dim3((unsigned)((P.N + 16 * NG - 1) / (16 * NG))),
+                     dim3(64 * W), 0, st, P);
   return hipGetLastError();
 }
 
@@ -279,8 +291,9 @@ hipError_t launch(const Args& P, hipStream_t st) {
 // sums are exact, so the split does not show in the result).
 namespace ring {
 
-template <int WM_, int WN_, int TM_, int TN_, int NS_, int SP_ = 4>
+template <int WM_, int WN_, int TM_, int TN_, int NS_, int SP_ = 4, int NTB_ = 0>
 struct G {
+  static constexpr int NTB = NTB_;  // B is read once: do not keep it in the caches
   static constexpr int SP = SP_;  // k-steps that a k-tile's DMAs are spread over
   static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NS = NS_;
   static constexpr int NW = WM * WN, NT = 64 * NW;
@@ -288,7 +301,7 @@ struct G {
   static constexpr int NB = (BM + BN) / 8 / NW;  // DMA blocks (8 rows) per wave and k-tile
   static constexpr int STAGE = (BM + BN) * KB;
   static_assert((BM + BN) % (8 * NW) == 0, "DMA blocks divide over the waves");
-  static_assert(NS >= 2 && NS <= 4 && (NS - 1) * NB < 64, "vmcnt range");
+  static_assert(NS >= 2 && NS <= 6 && (NS - 1) * NB < 64, "vmcnt range");
 };
 
 template <class T>
@@ -309,7 +322,10 @@ __device__ __forceinline__ void fetch(uint8_t* st, rsrc_t ra, rsrc_t rb, rsrc_t 
 #pragma unroll
   for (int u = U0; u < U1; ++u) {
     const int blk = T::NW * u + wave;  // uniform: blocks of A, then of B
-    dma<16>(!live ? none : 8 * blk < T::BM ? ra : rb, st + blk * 1024, L.off[u], ko);
+    if (8 * blk < T::BM)
+      dma<16>(live ? ra : none, st + blk * 1024, L.off[u], ko);
+    else
+      dma<16, T::NTB>(live ? rb : none, st + blk * 1024, L.off[u], ko);
   }
 }
 
@@ -350,8 +366,11 @@ __device__ __forceinline__ void interleave() {
 template <class T, int OUT>
 __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* part) {
   constexpr int NS = T::NS, NB = T::NB;
-  __shared__ __attribute__((aligned(16))) uint8_t s0[T::STAGE], s1[T::STAGE], s2[NS > 2 ? T::STAGE : 16],
-      s3[NS > 3 ? T::STAGE : 16];
+  // separate arrays: the compiler sees that a DMA into one does not feed reads
+  // of another, and adds no waits
+  __shared__ __attribute__((aligned(16))) uint8_t s0[T::STAGE], s1[T::STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s2[NS > 2 ? T::STAGE : 16], s3[NS > 3 ? T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s4[NS > 4 ? T::STAGE : 16], s5[NS > 5 ? T::STAGE : 16];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / T::WN, wn = wave % T::WN;
@@ -381,7 +400,9 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
 #pragma unroll
     for (int j = 0; j < T::TN; ++j) acc[i][j] = v16i{};
 
-  auto slot = [&](int s) { return s == 0 ? s0 : s == 1 ? s1 : s == 2 ? s2 : s3; };
+  auto slot = [&](int s) {
+    return s == 0 ? s0 : s == 1 ? s1 : s == 2 ? s2 : s == 3 ? s3 : s == 4 ? s4 : s5;
+  };
   // the first NS - 1 k-tiles and the first part of the next; the first k-tile
   // has landed when only the others' DMAs are outstanding
 #pragma unroll
@@ -398,7 +419,9 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
   // (each wave's own DMAs of it have landed, the later ones stay in flight)
   // and retires slot S (each wave's reads of it are done), which takes k-tile
   // k + NS: the first of its SP parts here, the others with the first k-steps
-  // of k-tile k + 1.
+  // of k-tile k + 1. (Fragments read two k-steps ahead, with the barrier in
+  // the middle, ran the 64 x 128 tile 4% faster and the larger ones 5-12%
+  // slower.)
   auto part_of = [&](auto S, auto Q, int k) {  // part Q of k-tile k into slot S
     constexpr int u0 = NB * Q.value / T::SP, u1 = NB * (Q.value + 1) / T::SP;
     if constexpr (Q.value < T::SP)
@@ -443,6 +466,14 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
     if constexpr (NS > 3) {
       step(std::integral_constant<int, 3>{}, k + 3);
       if (k + 4 >= nk) break;
+    }
+    if constexpr (NS > 4) {
+      step(std::integral_constant<int, 4>{}, k + 4);
+      if (k + 5 >= nk) break;
+    }
+    if constexpr (NS > 5) {
+      step(std::integral_constant<int, 5>{}, k + 5);
+      if (k + 6 >= nk) break;
     }
   }
   wait_vm<0>();  // the last (empty) DMAs still write LDS: let them land
@@ -790,18 +821,11 @@ bool fast_ok(const Args& P) {
 }
 
 // ----------------------------------------------------------- choice
-// The largest tile that still gives at least kFill tiles, that is work for
-// most of the 256 CUs; measured at K = 4096, N = 6144 (us, 64 x 128 / 128 x
-// 128 / 128 x 256 / 256 x 256 tiles): M = 256 16.7 / 19.7 / 30.0 / 39.9, M =
-// 512 30.9 / 21.3 / 30.4 / 39.9, M = 1024 48.7 / 41.8 / 34.9 / 40.3, M = 2048
-// 95.7 / 70.9 / 68.0 / 47.7. Where even the smallest tile gives fewer, k is
-// split to fill the CUs, with at least kMinTiles k-tiles a split (4096 x 14336
-// weight, M = 128: 42.3 unsplit, 26.2 in two, 21.4 in four).
-typedef ring::G<2, 4, 1, 1, 4, 3> R64x128;
+typedef ring::G<2, 4, 1, 1, 6, 3> R64x128;
+typedef ring::G<2, 4, 1, 1, 6, 3, 1> R64x128nt;
 typedef ring::G<4, 4, 1, 1, 4, 2> R128x128;
 typedef ring::G<4, 4, 1, 2, 3, 3> R128x256;
 
-constexpr int64_t kCUs = 256, kFill = 160, kMinTiles = 4, kMaxSplits = 16;
 enum Kind { kFew, k64x128, k128x128, k128x256, k256x256 };
 
 struct Plan {
@@ -809,23 +833,50 @@ struct Plan {
   int splits;
 };
 
-int64_t tiles_of(int64_t M, int64_t N, int64_t bm, int64_t bn) {
-  return ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+// The kernel with the least expected time, in us, by a model whose constants
+// were fitted to every kernel's and split's time at 90 sizes (1 to 2048 tokens,
+// weights of 200 x 1000 to 28672 x 4096): its choice is within 0.3% of the
+// fastest on average and 11% at worst. A few tokens: a start, and for each 4096
+// rows of B (16 a CU) and 1024 k a time that grows with M. Tiles: a start, and
+// for each round of 256 tiles c a k-tile, but no faster than B from memory,
+// the operands of all tiles through the caches, or the arithmetic; a split of
+// k adds a launch and its partial sums. Measured, for example, at 1024 x 4096
+// (N x K) and 64 tokens: few 11.9, 64 x 128 tiles 13.6, split in eight 8.9; at
+// 6144 x 4096 and 512 tokens 32.5 / 22.7 / 30.4 / 39.9 for the four tiles, and
+// at 1024 tokens 51.5 / 45.2 / 35.9 / 40.3.
+float tiled_us(int64_t M, int64_t N, int64_t K, int bm, int bn, float c, int splits) {
+  const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn), nk = K / KB;
+  const int64_t rounds = (tiles * splits + 255) / 256;
+  float t = (float)(rounds * ((nk + splits - 1) / splits)) * c;
+  t = fmaxf(t, (float)N * K / 13e6f);
+  t = fmaxf(t, (float)(tiles * nk) * ((bm + bn) * KB) / 14e6f);
+  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 3.5e9f);
+  return 5.6f + t + (splits > 1 ? 2.6f + (float)splits * M * N * 8.f / 5.8e6f : 0.f);
 }
 
+// Two groups of 16 rows of B to each load of A, where that leaves enough
+// work-groups (6144 x 4096, M = 16: 9.2 against 10.9 us; M = 1: 8.0, 8.0).
+bool two_groups(int64_t M, int64_t N) { return N >= 6144 && M > 4 && M <= 16; }
+
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  // Few tokens: no LDS staging, one launch (M = 4, us against the ring's best:
-  // 4096 x 14336 weight 13.8 / 15.8, 28672 x 4096 24.5 / 28.5, 1024 x 4096 4.9 /
-  // 8.6; at M = 16 18.6 / 15.9, 34.9 / 29.3 and 6.0 / 8.5).
-  if (M <= 8 || (M <= 16 && N * K <= (int64_t(1) << 24))) return {kFew, 1};
-  if (tiles_of(M, N, 256, 256) >= kFill) return {k256x256, 1};
-  if (tiles_of(M, N, 128, 256) >= kFill) return {k128x256, 1};
-  if (tiles_of(M, N, 128, 128) >= kFill) return {k128x128, 1};
-  const int64_t t = tiles_of(M, N, 64, 128), nk = K / KB;
-  int64_t s = t >= kFill ? 1 : kCUs / t;
-  s = s < nk / kMinTiles ? s : nk / kMinTiles;
-  s = s < kMaxSplits ? s : kMaxSplits;
-  return {k64x128, (int)(s > 1 ? s : 1)};
+  Plan best{k256x256, 1};
+  float t = tiled_us(M, N, K, 256, 256, 0.94f, 1);
+  const auto offer = [&](Kind kind, int splits, float us) {
+    if (us < t) {
+      t = us;
+      best = {kind, splits};
+    }
+  };
+  offer(k128x256, 1, tiled_us(M, N, K, 128, 256, 0.60f, 1));
+  offer(k128x128, 1, tiled_us(M, N, K, 128, 128, 0.45f, 1));
+  for (int s : {1, 2, 3, 4, 6, 8})  // splits of at least 4 k-tiles
+    if (s == 1 || s * 4 <= K / KB) offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.33f, s));
+  if (M <= 64) {
+    const float per = 0.71f + 0.033f * M * (two_groups(M, N) ? 0.75f : 1.f);
+    const float rows = (float)((N + 4095) / 4096);
+    offer(kFew, 1, 2.1f + fmaxf(rows * (float)K / 1024.f * per, (float)N * K / 13e6f));
+  }
+  return best;
 }
 
 template <int OUT>
@@ -833,8 +884,19 @@ hipError_t launch_out(const Args& P, void* ws, hipStream_t st) {
   if (!fast_ok(P)) return gen::launch<OUT>(P, st);
   const Plan plan = plan_of(P.M, P.N, P.K);
   switch (plan.kind) {
-    case kFew: return few::launch<8, 4, 1, OUT>(P, st);
-    case k64x128: return ring::launch<R64x128, OUT>(P, plan.splits, ws, st);
+    case kFew:
+      if (P.M > 32) return few::launch<8, 2, 4, 1, OUT>(P, st);
+      if (P.M > 16) return few::launch<8, 4, 2, 1, OUT>(P, st);
+      if (two_groups(P.M, P.N)) return few::launch<4, 8, 1, 2, OUT>(P, st);
+      return few::launch<8, 4, 1, 1, OUT>(P, st);
+    case k64x128:
+      // One tile-row reads B once. A large weight comes from HBM each time, and
+      // past the caches is faster (28672 x 4096, M = 64: 29.9 against 33.2 us);
+      // a smaller one may still lie in the 256 MB cache (6144 x 4096, used
+      // again after two others of its size: 12.8 kept against 16.3).
+      if (P.M <= 64 && P.N * P.K >= (int64_t(1) << 26))
+        return ring::launch<R64x128nt, OUT>(P, plan.splits, ws, st);
+      return ring::launch<R64x128, OUT>(P, plan.splits, ws, st);
     case k128x128: return ring::launch<R128x128, OUT>(P, 1, ws, st);
     case k128x256: return ring::launch<R128x256, OUT>(P, 1, ws, st);
     default: return big::launch<OUT>(P, st);
