@@ -425,8 +425,9 @@ int mxfp4_int8_quantize(const void* x, int64_t x_ld, const void* gate, int64_t g
  * on the kernel that serves it. A scale of NaN makes its row or column NaN. Operands that are
  * 16-byte aligned with pitches that are multiples of 16, and K % 128 == 0
  * (what the quantizers' zero codes allow for any width), take the fast
- * kernels. ws: mxfp4_int8_gemm_workspace_bytes(M, N, K) bytes, 16-byte
- * aligned (may be 0, then ws may be NULL).
+ * kernels. M and N are below 2^26, with at most 2^23 tiles of 64 x 64 in C. ws:
+ * mxfp4_int8_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned (may be 0,
+ * then ws may be NULL).
  */
 int mxfp4_int8_gemm(const void* A, int64_t lda, const float* a_scales, const void* B, int64_t ldb,
                     const float* b_scales, const float* bias, int64_t M, int64_t N, int64_t K,

@@ -11,7 +11,8 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 31;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxK = 131071;               // 2^14 K < 2^31: the int32 sums stay exact
-constexpr int64_t kMaxTiles = int64_t(1) << 24; // 64 x 64 tiles of C: 2^32 threads in a grid
+constexpr int64_t kMaxDim = int64_t(1) << 26;   // a product's rows of A and of B, and
+constexpr int64_t kMaxTiles = int64_t(1) << 23; // its 64 x 64 tiles: grids stay below 2^32 threads
 
 bool valid_dtype(int t) { return t >= MXFP4_DT_F32 && t <= MXFP4_DT_F16; }
 int size_of(int t) { return t == MXFP4_DT_F32 ? 4 : 2; }
@@ -120,7 +121,7 @@ int mxfp4_int8_quantize(const void* x, int64_t x_ld, const void* gate, int64_t g
 }
 
 static bool gemm_sizes_ok(int64_t M, int64_t N, int64_t K) {
-  if (M < 0 || N < 0 || K < 1 || K > kMaxK || M >= kMaxRows || N >= kMaxRows) return false;
+  if (M < 0 || N < 0 || K < 1 || K > kMaxK || M >= kMaxDim || N >= kMaxDim) return false;
   const int64_t tm = (M + 63) / 64, tn = (N + 63) / 64;
   return tn == 0 || tm < kMaxTiles / tn;
 }

@@ -233,7 +233,7 @@ __global__ __launch_bounds__(64 * W) void gemm_kernel(Args P) {
     const uint32_t so = (uint32_t)c * 64;
 #pragma unroll
     for (int h = 0; h < NG; ++h)
-      qb[u][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, vb[h] | dead, so, 2));
+      qb[u][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, vb[h] | dead, so, 0));
 #pragma unroll
     for (int g = 0; g < MG; ++g)
       qa[u][g] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, va[g] | dead, so, 0));
@@ -833,48 +833,51 @@ struct Plan {
   int splits;
 };
 
-// The kernel with the least expected time, in us, by a model whose constants
-// were fitted to every kernel's and split's time at 90 sizes (1 to 2048 tokens,
-// weights of 200 x 1000 to 28672 x 4096): its choice is within 0.3% of the
-// fastest on average and 11% at worst. A few tokens: a start, and for each 4096
-// rows of B (16 a CU) and 1024 k a time that grows with M. Tiles: a start, and
-// for each round of 256 tiles c a k-tile, but no faster than B from memory,
+// The kernel and split with the least expected time, in us, by a model whose
+// constants were fitted to the times of all of them at 135 sizes (1 to 4096
+// tokens, weights of 155 x 1664 to 28672 x 4096): its choice is within 0.4% of
+// the fastest on average, 10% at worst. Few tokens: a start, and for each
+// round of 256 work-groups and 1024 k a time that grows with M. Tiles: a start,
+// and for each round of 256 tiles c a k-tile, but no faster than B from memory,
 // the operands of all tiles through the caches, or the arithmetic; a split of
 // k adds a launch and its partial sums. Measured, for example, at 1024 x 4096
-// (N x K) and 64 tokens: few 11.9, 64 x 128 tiles 13.6, split in eight 8.9; at
+// (N x K) and 64 tokens: few 10.8, 64 x 128 tiles 14.3, split in eight 8.6; at
 // 6144 x 4096 and 512 tokens 32.5 / 22.7 / 30.4 / 39.9 for the four tiles, and
 // at 1024 tokens 51.5 / 45.2 / 35.9 / 40.3.
 float tiled_us(int64_t M, int64_t N, int64_t K, int bm, int bn, float c, int splits) {
   const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn), nk = K / KB;
   const int64_t rounds = (tiles * splits + 255) / 256;
   float t = (float)(rounds * ((nk + splits - 1) / splits)) * c;
-  t = fmaxf(t, (float)N * K / 13e6f);
+  t = fmaxf(t, (float)N * K / 5.7e6f);
   t = fmaxf(t, (float)(tiles * nk) * ((bm + bn) * KB) / 14e6f);
-  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 3.5e9f);
-  return 5.6f + t + (splits > 1 ? 2.6f + (float)splits * M * N * 8.f / 5.8e6f : 0.f);
+  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 2.1e9f);
+  return 5.f + t + (splits > 1 ? 1.9f + (float)splits * M * N * 8.f / 2.7e6f : 0.f);
 }
 
-// Two groups of 16 rows of B to each load of A, where that leaves enough
-// work-groups (6144 x 4096, M = 16: 9.2 against 10.9 us; M = 1: 8.0, 8.0).
-bool two_groups(int64_t M, int64_t N) { return N >= 6144 && M > 4 && M <= 16; }
+// Two groups of 16 rows of B to each load of A where that still gives most CUs
+// a work-group (us, one group / two: 6144 x 4096, M = 4 8.8 / 6.9, M = 16 10.2 /
+// 7.9, M = 64 20.0 / 14.0; 1024 x 4096, M = 16 5.4 / 7.4).
+bool two_groups(int64_t N) { return N > 4608; }
 
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   Plan best{k256x256, 1};
-  float t = tiled_us(M, N, K, 256, 256, 0.94f, 1);
+  float t = tiled_us(M, N, K, 256, 256, 1.3f, 1);
   const auto offer = [&](Kind kind, int splits, float us) {
     if (us < t) {
       t = us;
       best = {kind, splits};
     }
   };
-  offer(k128x256, 1, tiled_us(M, N, K, 128, 256, 0.60f, 1));
-  offer(k128x128, 1, tiled_us(M, N, K, 128, 128, 0.45f, 1));
-  for (int s : {1, 2, 3, 4, 6, 8})  // splits of at least 4 k-tiles
-    if (s == 1 || s * 4 <= K / KB) offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.33f, s));
+  for (int s : {1, 2, 3, 4, 6, 8}) {  // splits of at least 4 k-tiles
+    if (s > 1 && (s * 4 > K / KB || M > 4096)) break;  // (rows are a grid dimension of the sums)
+    if (s <= 2) offer(k128x256, s, tiled_us(M, N, K, 128, 256, 1.1f, s));
+    if (s <= 4) offer(k128x128, s, tiled_us(M, N, K, 128, 128, 0.77f, s));
+    offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.45f, s));
+  }
   if (M <= 64) {
-    const float per = 0.71f + 0.033f * M * (two_groups(M, N) ? 0.75f : 1.f);
-    const float rows = (float)((N + 4095) / 4096);
-    offer(kFew, 1, 2.1f + fmaxf(rows * (float)K / 1024.f * per, (float)N * K / 13e6f));
+    const int64_t rows = two_groups(N) ? 8192 : 4096;  // 256 work-groups' rows of B
+    const float per = (0.59f + 0.027f * M) * (two_groups(N) ? 1.7f : 1.f);
+    offer(kFew, 1, 2.8f + fmaxf((float)((N + rows - 1) / rows) * K / 1024.f * per, (float)N * K / 5.7e6f));
   }
   return best;
 }
@@ -885,20 +888,21 @@ hipError_t launch_out(const Args& P, void* ws, hipStream_t st) {
   const Plan plan = plan_of(P.M, P.N, P.K);
   switch (plan.kind) {
     case kFew:
-      if (P.M > 32) return few::launch<8, 2, 4, 1, OUT>(P, st);
-      if (P.M > 16) return few::launch<8, 4, 2, 1, OUT>(P, st);
-      if (two_groups(P.M, P.N)) return few::launch<4, 8, 1, 2, OUT>(P, st);
-      return few::launch<8, 4, 1, 1, OUT>(P, st);
+      if (P.M <= 16)
+        return two_groups(P.N) ? few::launch<8, 4, 1, 2, OUT>(P, st) : few::launch<8, 4, 1, 1, OUT>(P, st);
+      if (P.M <= 32)
+        return two_groups(P.N) ? few::launch<4, 4, 2, 2, OUT>(P, st) : few::launch<8, 4, 2, 1, OUT>(P, st);
+      return two_groups(P.N) ? few::launch<4, 4, 4, 2, OUT>(P, st) : few::launch<8, 2, 4, 1, OUT>(P, st);
     case k64x128:
       // One tile-row reads B once. A large weight comes from HBM each time, and
-      // past the caches is faster (28672 x 4096, M = 64: 29.9 against 33.2 us);
+      // past the caches is faster (28672 x 4096, M = 64: 29.0 against 33.9 us);
       // a smaller one may still lie in the 256 MB cache (6144 x 4096, used
-      // again after two others of its size: 12.8 kept against 16.3).
+      // again after two others of its size: 15.9 kept against 21.0).
       if (P.M <= 64 && P.N * P.K >= (int64_t(1) << 26))
         return ring::launch<R64x128nt, OUT>(P, plan.splits, ws, st);
       return ring::launch<R64x128, OUT>(P, plan.splits, ws, st);
-    case k128x128: return ring::launch<R128x128, OUT>(P, 1, ws, st);
-    case k128x256: return ring::launch<R128x256, OUT>(P, 1, ws, st);
+    case k128x128: return ring::launch<R128x128, OUT>(P, plan.splits, ws, st);
+    case k128x256: return ring::launch<R128x256, OUT>(P, plan.splits, ws, st);
     default: return big::launch<OUT>(P, st);
   }
 }

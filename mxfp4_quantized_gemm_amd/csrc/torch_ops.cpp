@@ -36,9 +36,18 @@ void check(int status, const char* where) {
   throw py::error_already_set();
 }
 
+// The codes have no gradient: a call that autograd would have to record is refused.
+void no_gradient(const char* where, std::initializer_list<const Tensor*> inputs) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const Tensor* t : inputs)
+    TORCH_CHECK(t == nullptr || !t->requires_grad(), where,
+                " has no gradient: call it under torch.no_grad() or on detached tensors");
+}
+
 hipStream_t stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.device().index()).stream(); }
 
 bool has(const Maybe& t) { return t.has_value() && t->defined(); }
+const Tensor* ptr(const Maybe& t) { return has(t) ? &*t : nullptr; }
 
 void on_gpu(const Tensor& t, const char* name, const Tensor* like = nullptr) {
   TORCH_CHECK_VALUE(t.is_cuda(), name, " must live in GPU memory");
@@ -204,6 +213,7 @@ Operand new_operand(const Rows& x) {
 }
 
 Operand norm_int8(const Tensor& x, const Maybe& weight, double eps, const Maybe& residual, Tensor* h) {
+  no_gradient("rms_norm_int8", {&x, ptr(weight), ptr(residual)});
   const Norm n(x, residual, weight);
   const c10::DeviceGuard guard(x.device());
   Operand o = new_operand(n.x);
@@ -223,6 +233,7 @@ py::tuple rms_norm_int8(const Tensor& x, const Maybe& weight, double eps, const 
 
 // ------------------------------------------------------------ 8 bits
 Operand quantize(const Tensor& x, const Maybe& gate) {
+  no_gradient("int8_quantize", {&x, ptr(gate)});
   if (has(gate)) TORCH_CHECK_VALUE(gate->sizes() == x.sizes(), "gate must be ", x.sizes(), ", got ", gate->sizes());
   on_gpu(x, "x");
   const int dtype = dtype_of(x, "x");

@@ -132,6 +132,8 @@ def test_gemm_refusals(lib):
     assert call(ldb=63) == ESHAPE
     assert call(ldc=7) == ESHAPE
     assert call(M=1 << 20, N=1 << 20, ldc=1 << 20) == ESHAPE  # more tiles than a grid has
+    assert call(N=1 << 26, ldc=1 << 26) == ESHAPE
+    assert call(M=1 << 26) == ESHAPE
     for k in ("A", "sa", "B", "sb", "C"):
         assert call(**{k: NULL}) == ENULL, k
     assert call(sa=TWO) == EALIGN
@@ -170,3 +172,15 @@ def test_wrappers_refuse_cpu_tensors_and_wrong_shapes():
         int8.Int8Linear(32, 16)(x)
     with pytest.raises(ValueError, match="columns"):
         int8.int8_linear(x, torch.zeros(8, 100, dtype=torch.int8), s)
+
+
+def test_calls_without_a_gradient_refuse_to_be_recorded():
+    from mxfp4_quantized_gemm_amd import int8, norm
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, requires_grad=True)
+    q, s = torch.zeros(4, 128, dtype=torch.int8), torch.ones(4)
+    for call in (lambda: int8.int8_quantize(x), lambda: norm.rms_norm_int8(x), lambda: int8.int8_linear(x, q, s),
+                 lambda: int8.int8_quantize(x.detach(), gate=x), lambda: norm.rms_norm_int8(x.detach(), residual=x)):
+        with pytest.raises(RuntimeError, match="no gradient"):
+            call()
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU memory"):
+        int8.int8_quantize(x)
