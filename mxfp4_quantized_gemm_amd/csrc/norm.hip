@@ -317,13 +317,19 @@ struct BwdArgs {
   bool wide;
 };
 
-// Work-groups walk rows blockIdx.x, + gridDim.x, ...: the weight's gradient
-// is summed over a work-group's rows in registers, and the work-groups'
-// partial sums by a second kernel in a fixed order (no atomics).
+// Work-groups walk the rows in turn (with one wave a row, four rows at a time):
+// the weight's gradient is summed over a work-group's rows in registers, and
+// the work-groups' partial sums by a second kernel, in a fixed order (no
+// atomics). One work-group's partial sums cost as much traffic as two rows in
+// 16 bits, so there are no more of them than keep the loads going: 8192 x 4096
+// bf16 took 62.2 us with 1024 work-groups of 256 threads and 58.2 with 512,
+// 4096 x 16384 146 with 1024 of 1024 threads and 112 with 256.
 template <int T, int V, int TPR, int R>
-__global__ __launch_bounds__(TPR) void bwd_kernel(BwdArgs A) {
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void bwd_kernel(BwdArgs A) {
+  constexpr int RPG = TPR < 256 ? 256 / TPR : 1;  // rows at a time
   __shared__ float red[2][TPR / 64];
-  const int t = threadIdx.x;
+  __shared__ float meet[RPG > 1 ? RPG * TPR * R * V : 1];
+  const int t = threadIdx.x % TPR, part = threadIdx.x / TPR;
   typedef Row<T, V, TPR, R> X;
   float w[R][V], dw[R][V];
   load_weight<T, V, TPR, R>(A.w, A.wide, A.cols, t, w);
@@ -332,7 +338,8 @@ __global__ __launch_bounds__(TPR) void bwd_kernel(BwdArgs A) {
 #pragma unroll
     for (int k = 0; k < V; ++k) dw[i][k] = 0.f;
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = (int64_t)blockIdx.x * RPG + part; row < A.rows;
+       row += (int64_t)gridDim.x * RPG, turn ^= 1) {
     float g[R][V], u[R][V];
     X::load(A.dy, row * A.dy_ld, A.cols, t, g);
     X::load(A.h, row * A.h_ld, A.cols, t, u);
@@ -365,7 +372,20 @@ __global__ __launch_bounds__(TPR) void bwd_kernel(BwdArgs A) {
       for (int k = 0; k < V; ++k) d[i][k] = fmaf(r, g[i][k] - u[i][k] * s, d[i][k]);
     X::store(A.dx, row * A.dx_ld, A.cols, t, d);
   }
-  if (A.part != nullptr) {
+  if (A.part == nullptr) return;
+  if constexpr (RPG > 1) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) meet[part * TPR * R * V + (t + TPR * i) * V + k] = dw[i][k];
+    __syncthreads();
+    for (int c = threadIdx.x; c < A.cols; c += 256) {
+      float v = meet[c];
+#pragma unroll
+      for (int q = 1; q < RPG; ++q) v += meet[q * TPR * R * V + c];
+      A.part[(int64_t)blockIdx.x * A.cols + c] = v;
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -376,23 +396,23 @@ __global__ __launch_bounds__(TPR) void bwd_kernel(BwdArgs A) {
   }
 }
 
-// dw[c] = sum over the parts p of part[p][c]: 16 waves of a work-group take
-// every 16th part of 64 columns, then their sums meet in order.
+// dw[c] = sum over the parts p of part[p][c]: 32 half-waves of a work-group
+// take every 32nd part of 32 columns, then their sums meet in order.
 template <int T>
 __global__ __launch_bounds__(1024) void dw_kernel(const float* part, int parts, int cols, void* dw) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  __shared__ float red[32][32];
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = wave; p < parts; p += 16) s += part[(int64_t)p * cols + c];
+    for (int p = q; p < parts; p += 32) s += part[(int64_t)p * cols + c];
   }
-  red[wave][lane] = s;
+  red[q][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < cols) {
+  if (q == 0 && c < cols) {
 #pragma unroll
-    for (int k = 1; k < 16; ++k) s += red[k][lane];
+    for (int k = 1; k < 32; ++k) s += red[k][lane];
     put1<T>(dw, c, s);
   }
 }
@@ -444,25 +464,24 @@ hipError_t go_type(const RowArgs& A, int dtype, hipStream_t st) {
   }
 }
 
-// Work-groups of the gradient: 16 waves a CU (work-groups are of one or two
-// waves up to 1024 columns, of four or more above), few enough that their
-// partial sums stay small beside the rows themselves.
+// Work-groups of the gradient, of 4 waves up to 4096 columns and 16 above.
 int64_t bwd_groups(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 1024 ? 4096 : 1024;
-  return rows < most ? rows : most;
+  const int64_t most = cols <= 4096 ? 512 : 256;
+  const int64_t need = cols <= 1024 ? (rows + 3) / 4 : rows;
+  return need < most ? need : most;
 }
 
 template <int T, int V, int TPR, int E>
 hipError_t go_bwd(const BwdArgs& A, hipStream_t st) {
-  hipLaunchKernelGGL((bwd_kernel<T, V, TPR, E / V>), dim3((unsigned)bwd_groups(A.rows, A.cols)), dim3(TPR),
-                     0, st, A);
+  hipLaunchKernelGGL((bwd_kernel<T, V, TPR, E / V>), dim3((unsigned)bwd_groups(A.rows, A.cols)),
+                     dim3(TPR < 256 ? 256 : TPR), 0, st, A);
   return hipGetLastError();
 }
 
 template <int T, int V>
 hipError_t go_bwd_width(const BwdArgs& A, hipStream_t st) {
   if (A.cols <= 512) return go_bwd<T, V, 64, 8>(A, st);
-  if (A.cols <= 1024) return go_bwd<T, V, 128, 8>(A, st);
+  if (A.cols <= 1024) return go_bwd<T, V, 64, 16>(A, st);
   if (A.cols <= 4096) return go_bwd<T, V, 256, 16>(A, st);
   if (A.cols <= 16384) return go_bwd<T, V, 1024, 16>(A, st);
   return go_bwd<T, V, 1024, 32>(A, st);
@@ -521,7 +540,7 @@ hipError_t launch_rmsnorm_bwd(CMat dy, CMat dh, CMat h, const void* weight, int 
     if (e != hipSuccess) return e;
   }
   if (dweight == nullptr) return hipSuccess;
-  const dim3 grid((unsigned)((cols + 63) / 64)), blk(1024);
+  const dim3 grid((unsigned)((cols + 31) / 32)), blk(1024);
   const int parts = (int)bwd_groups(rows, cols);
   const float* p = static_cast<const float*>(ws);
   if (weight_dtype == kBF16)
