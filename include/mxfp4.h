@@ -357,9 +357,8 @@ size_t mxfp4_workspace_bytes(int op, int64_t T, int64_t N, int64_t K);
  *
  * Conventions beside those at the top of this file: `dtype` (and out_dtype)
  * is an mxfp4_dtype; matrices are row-major with a row pitch `ld` in
- * elements, ld >= cols (any pitch and any alignment to the element's size is
- * accepted; 16-byte aligned rows whose width is a multiple of 16 bytes are
- * read 16 bytes at a time). The outputs' memory must not overlap the inputs',
+ * elements, ld >= cols (any pitch, and any alignment to the element's size).
+ * The outputs' memory must not overlap the inputs',
  * except that h may be x or residual itself. rows == 0 (M or N == 0) is a
  * valid empty call. All results are deterministic.
  *
