@@ -199,6 +199,174 @@ __device__ __forceinline__ void tile_of(int64_t wg, int64_t nwg, int64_t ntm, in
   tn = r / gs;
 }
 
+// ------------------------------------------------------------- epilogue
+// The tiled kernels give the MFMA the weight's rows first, so that a lane's
+// registers 4 q .. 4 q + 3 are four consecutive columns (8 q + 4 (lane / 32)) of
+// row lane % 32 of C. Tiles go out through LDS, each wave its own 2.5 KiB:
+// lanes then store 16 bytes each of 64 or 128 consecutive bytes of a row, at
+// any alignment. (8192 x 28672 x 4096 bf16, us: 128-byte rows 830, 64-byte rows
+// 872, 4-byte stores straight from the registers after exchanges between
+// lanes 843; with a width of 4097 164 / 196 / 168. Kept in the caches instead
+// of past them 848. The middle sizes gained from 64-byte rows over 2-byte
+// stores: 1024 x 6144 x 4096 35.9 -> 32.6, 512 x 4096 x 4096 32.5 -> 29.2.)
+constexpr int kI32 = 3;                  // partial sums of a split of k
+constexpr int kStage = 32 * (64 + 16);   // rows padded by 16 bytes: banks spread
+
+// A tile's scales and bias in LDS, filled by DMA (rows past the end are 0).
+struct Factors {
+  const float *sa, *sb, *bias;
+};
+
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// Staged rows of RB bytes (32 of 64 or 16 of 128) to C from row m0, column n0.
+template <int OUT, int RB>
+__device__ __forceinline__ void store_rows(const uint8_t* stage, void* C, int64_t ldc, int64_t m0,
+                                           int64_t n0, int64_t M, int64_t N, int lane) {
+  typedef u32x4 u32x4_2 __attribute__((aligned(2)));  // C may start at any element
+  constexpr int S = OUT == kBF16 || OUT == kF16 ? 2 : 4, V = 16 / S, L = RB / 16;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 64 / L * h + lane / L;
+    const u32x4 q = *reinterpret_cast<const u32x4*>(stage + r * (RB + 16) + lane % L * 16);
+    const int64_t m = m0 + r, n = n0 + lane % L * V;
+    uint8_t* p = static_cast<uint8_t*>(C) + (m * ldc + n) * S;
+    if (m < M && n + V <= N) {
+      if constexpr (OUT == kI32)
+        *reinterpret_cast<u32x4_2*>(p) = q;  // read again soon
+      else
+        __builtin_nontemporal_store(q, reinterpret_cast<u32x4_2*>(p));
+    } else if (m < M) {
+#pragma unroll
+      for (int e = 0; e < V - 1; ++e) {
+        const uint32_t d = q[e * S / 4];
+        if (n + e < N) {
+          if constexpr (S == 4)
+            reinterpret_cast<uint32_t*>(p)[e] = d;
+          else
+            reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(d >> (16 * (e & 1)));
+        }
+      }
+    }
+  }
+}
+
+// The lane's four columns of group q of a tile, scaled: 16 bits or 32 each.
+template <int OUT>
+__device__ __forceinline__ u32x4 four(const v16i& acc, int q, float sa, Factors F, int half) {
+  const float4 sb = *reinterpret_cast<const float4*>(F.sb + 8 * q + 4 * half);
+  const float4 b = *reinterpret_cast<const float4*>(F.bias + 8 * q + 4 * half);
+  const float v0 = scaled(acc[4 * q], sa, sb.x, b.x), v1 = scaled(acc[4 * q + 1], sa, sb.y, b.y);
+  const float v2 = scaled(acc[4 * q + 2], sa, sb.z, b.z), v3 = scaled(acc[4 * q + 3], sa, sb.w, b.w);
+  if constexpr (OUT == kF32)
+    return u32x4{__float_as_uint(v0), __float_as_uint(v1), __float_as_uint(v2), __float_as_uint(v3)};
+  else
+    return u32x4{pack2<OUT>(v0, v1), pack2<OUT>(v2, v3), 0, 0};
+}
+
+// One tile (rows m0 .., columns n0 ..) of C, 64 bytes of every row at a time;
+// its rows' scales start at F.sa, its columns' at F.sb and F.bias (not read
+// for partial sums). `stage` is the wave's own.
+template <int OUT>
+__device__ __forceinline__ void put_tile(const v16i& acc, uint8_t* stage, Factors F, void* C, int64_t ldc,
+                                         int64_t m0, int64_t n0, int64_t M, int64_t N, int lane) {
+  const int half = lane >> 5, l32 = lane & 31;
+  uint8_t* row = stage + l32 * (64 + 16);
+  if constexpr (OUT == kBF16 || OUT == kF16) {
+    const float sa = F.sa[l32];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const u32x4 d = four<OUT>(acc, q, sa, F, half);
+      *reinterpret_cast<u32x2*>(row + 16 * q + 8 * half) = u32x2{d.x, d.y};
+    }
+    wave_sync();
+    store_rows<OUT, 64>(stage, C, ldc, m0, n0, M, N, lane);
+    wave_sync();
+  } else {
+    const float sa = OUT == kI32 ? 0.f : F.sa[l32];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {  // 16 columns each
+#pragma unroll
+      for (int q = 2 * p; q < 2 * p + 2; ++q) {
+        u32x4 d;
+        if constexpr (OUT == kI32)
+          d = u32x4{(uint32_t)acc[4 * q], (uint32_t)acc[4 * q + 1], (uint32_t)acc[4 * q + 2], (uint32_t)acc[4 * q + 3]};
+        else
+          d = four<OUT>(acc, q, sa, F, half);
+        *reinterpret_cast<u32x4*>(row + 32 * (q & 1) + 16 * half) = d;
+      }
+      wave_sync();
+      store_rows<OUT, 64>(stage, C, ldc, m0, n0 + 16 * p, M, N, lane);
+      wave_sync();
+    }
+  }
+}
+
+// Two tiles side by side, 128 bytes of 16 rows at a time: 64 columns of 16
+// bits, or each tile's 32 columns of 32 bits in turn.
+template <int OUT>
+__device__ __forceinline__ void put_pair(const v16i& acc0, const v16i& acc1, uint8_t* stage, Factors F, void* C,
+                                         int64_t ldc, int64_t m0, int64_t n0, int64_t M, int64_t N, int lane) {
+  const int half = lane >> 5, l32 = lane & 31;
+  const float sa = F.sa[l32];
+  const Factors F1{F.sa, F.sb + 32, F.bias + 32};
+  uint8_t* row = stage + (l32 & 15) * (128 + 16);
+  u32x4 d[2][4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) d[0][q] = four<OUT>(acc0, q, sa, F, half);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) d[1][q] = four<OUT>(acc1, q, sa, F1, half);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {  // rows 0-15, 16-31
+    if constexpr (OUT == kF32) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (l32 >> 4 == p) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) *reinterpret_cast<u32x4*>(row + 32 * q + 16 * half) = d[j][q];
+        }
+        wave_sync();
+        store_rows<OUT, 128>(stage, C, ldc, m0 + 16 * p, n0 + 32 * j, M, N, lane);
+        wave_sync();
+      }
+    } else {
+      if (l32 >> 4 == p) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<u32x2*>(row + 64 * j + 16 * q + 8 * half) = u32x2{d[j][q].x, d[j][q].y};
+      }
+      wave_sync();
+      store_rows<OUT, 128>(stage, C, ldc, m0 + 16 * p, n0, M, N, lane);
+      wave_sync();
+    }
+  }
+}
+
+// Scales and bias of the BM rows from m0 and the BN columns from n0 to LDS
+// (sa, then sb, then bias; without a bias zeros), 64 of them an instruction.
+template <int BM, int BN, int NW>
+__device__ __forceinline__ void fetch_factors(uint8_t* lds, const Args& P, int64_t m0, int64_t n0,
+                                              rsrc_t none, int wave, int lane) {
+  const int64_t mb = min(P.M - m0, (int64_t)BM) * 4, nb = min(P.N - n0, (int64_t)BN) * 4;
+#pragma unroll
+  for (int u = 0; u < (BM + 2 * BN) / 64; u += NW) {
+    const int blk = u + wave;
+    if (blk < BM / 64)
+      dma<4>(make_rsrc(P.sa + m0, mb), lds + blk * 256, (blk * 64 + lane) * 4, 0);
+    else if (blk < (BM + BN) / 64)
+      dma<4>(make_rsrc(P.sb + n0, nb), lds + blk * 256, ((blk - BM / 64) * 64 + lane) * 4, 0);
+    else if (blk < (BM + 2 * BN) / 64)
+      dma<4>(P.bias ? make_rsrc(P.bias + n0, nb) : none, lds + blk * 256,
+             ((blk - (BM + BN) / 64) * 64 + lane) * 4, 0);
+  }
+}
+
 // ------------------------------------------------------- few tokens (M <= 16 MG)
 // The weight's bytes are the work. A work-group owns 16 rows of B and its W
 // waves split k: chunk c of 64 bytes of the 16 rows belongs to wave c % W,
@@ -322,7 +490,9 @@ __device__ __forceinline__ void fetch(uint8_t* st, rsrc_t ra, rsrc_t rb, rsrc_t 
 #pragma unroll
   for (int u = U0; u < U1; ++u) {
     const int blk = T::NW * u + wave;  // uniform: blocks of A, then of B
-    if (8 * blk < T::BM)
+    // (which of the two is known here where A's blocks divide over the waves)
+    const bool of_a = T::BM / 8 % T::NW == 0 ? u < T::BM / 8 / T::NW : 8 * blk < T::BM;
+    if (of_a)
       dma<16>(live ? ra : none, st + blk * 1024, L.off[u], ko);
     else
       dma<16, T::NTB>(live ? rb : none, st + blk * 1024, L.off[u], ko);
@@ -343,7 +513,7 @@ __device__ __forceinline__ void mul(const Frag<T>& F, v16i (&acc)[T::TM][T::TN])
   for (int i = 0; i < T::TM; ++i)
 #pragma unroll
     for (int j = 0; j < T::TN; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F.a[i], F.b[j], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F.b[j], F.a[i], acc[i][j], 0, 0, 0);
 }
 
 // Scheduling of a k-step: its LDS reads and DMAs spread over its MFMAs (left
@@ -371,6 +541,7 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
   __shared__ __attribute__((aligned(16))) uint8_t s0[T::STAGE], s1[T::STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t s2[NS > 2 ? T::STAGE : 16], s3[NS > 3 ? T::STAGE : 16];
   __shared__ __attribute__((aligned(16))) uint8_t s4[NS > 4 ? T::STAGE : 16], s5[NS > 5 ? T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t factors[(T::BM + 2 * T::BN) * 4];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / T::WN, wn = wave % T::WN;
@@ -403,8 +574,9 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
   auto slot = [&](int s) {
     return s == 0 ? s0 : s == 1 ? s1 : s == 2 ? s2 : s == 3 ? s3 : s == 4 ? s4 : s5;
   };
-  // the first NS - 1 k-tiles and the first part of the next; the first k-tile
-  // has landed when only the others' DMAs are outstanding
+  // the scales and bias, the first NS - 1 k-tiles and the first part of the
+  // next; the first k-tile has landed when only the others' DMAs are outstanding
+  if (splits == 1) fetch_factors<T::BM, T::BN, T::NW>(factors, P, m0, n0, none, wave, lane);
 #pragma unroll
   for (int k = 0; k < NS - 1; ++k)
     fetch<T>(slot(k), ra, rb, none, k < nk, L, (uint32_t)(k0 + k) * KB, wave);
@@ -476,27 +648,26 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
       if (k + 6 >= nk) break;
     }
   }
-  wait_vm<0>();  // the last (empty) DMAs still write LDS: let them land
-
-  const int half = lane >> 5, l32 = lane & 31;
+  // The last (empty) DMAs land and every wave is done with the slots: the
+  // first ones become the waves' staging of the epilogue.
+  wait_vm<0, true>();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  static_assert(T::NW * kStage <= 2 * T::STAGE, "staging fits two slots");
+  uint8_t* stage = wave * kStage + kStage <= T::STAGE ? s0 + wave * kStage : s1 + (wave - T::STAGE / kStage) * kStage;
+  const float* f = reinterpret_cast<const float*>(factors);
 #pragma unroll
-  for (int j = 0; j < T::TN; ++j) {
-    const int64_t n = n0 + (wn * T::TN + j) * 32 + l32;
-    if (n >= P.N) continue;
-    const bool whole = splits == 1;
-    const float sb = whole ? P.sb[n] : 0.f, bias = whole && P.bias ? P.bias[n] : 0.f;
+  for (int j = 0; j < T::TN; ++j)
 #pragma unroll
-    for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int64_t m = m0 + (wm * T::TM + i) * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
-        if (m >= P.M) continue;
-        if (whole)
-          put<OUT>(P.C, m * P.ldc + n, scaled(acc[i][j][e], P.sa[m], sb, bias));
-        else
-          part[((int64_t)z * P.M + m) * P.N + n] = acc[i][j][e];
-      }
-  }
+    for (int i = 0; i < T::TM; ++i) {
+      const int r = (wm * T::TM + i) * 32, c = (wn * T::TN + j) * 32;
+      const Factors F{f + r, f + T::BM + c, f + T::BM + T::BN + c};
+      if (splits == 1)
+        put_tile<OUT>(acc[i][j], stage, F, P.C, P.ldc, m0 + r, n0 + c, P.M, P.N, lane);
+      else
+        put_tile<kI32>(acc[i][j], stage, F, part + (int64_t)z * P.M * P.N, P.N, m0 + r, n0 + c, P.M, P.N, lane);
+    }
 }
 
 template <int OUT>
@@ -538,7 +709,7 @@ hipError_t launch(const Args& P, int splits, void* ws, hipStream_t st) {
 // epilogue waits for no load.
 namespace big {
 
-constexpr int BM = 256, BN = 256, TM = 4, TN = 2, WN = 4;
+constexpr int BM = 256, BN = 256, TM = 4, TN = 2, WN = 4;  // (put_pair takes the two)
 constexpr int TILE = BM * KB, STAGE = 2 * TILE;
 constexpr int DA = 4;  // DMA blocks of an operand per wave and k-tile
 
@@ -584,7 +755,7 @@ __device__ __forceinline__ void mul(const Frag& F, v16i (&acc)[TN][TM]) {
   for (int j = 0; j < TN; ++j)
 #pragma unroll
     for (int i = 0; i < TM; ++i)
-      acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F.a[i], F.b[j], acc[j][i], 0, 0, 0);
+      acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F.b[j], F.a[i], acc[j][i], 0, 0, 0);
 }
 
 // One MFMA, then an LDS read and a DMA where there are any left, and so on.
@@ -645,14 +816,14 @@ __device__ __forceinline__ Tile tile_at(const Args& P, int64_t vt, int64_t ntile
 
 template <int OUT>
 __global__ __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2)))
-void gemm_kernel(Args P, bool pairs) {
+void gemm_kernel(Args P) {
   __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
   __shared__ __attribute__((aligned(16))) float sc[2][3 * 256];  // sa, sb, bias of a tile
+  __shared__ __attribute__((aligned(16))) uint8_t staging[8 * kStage];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int half = lane >> 5, l32 = lane & 31;
   const int64_t ntm = (P.M + BM - 1) / BM, ntn = (P.N + BN - 1) / BN, ntiles = ntm * ntn;
   const int64_t step = gridDim.x;
   const int nk = (int)(P.K / KB), np = (nk + 1) & ~1;
@@ -692,91 +863,19 @@ void gemm_kernel(Args P, bool pairs) {
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int i = 0; i < TM; ++i) acc[j][i] = v16i{};
-    // waves 0-3: the rows' scales; 4-7: the columns' scales and bias. Read
-    // after the last k-tile, several barriers later; the buffers alternate,
-    // so no wave still reads the one that is filled.
-    {
-      uint8_t* s = reinterpret_cast<uint8_t*>(sc[turn]);
-      const int w = wave & 3;
-      if (wave < 4) {
-        dma<4>(make_rsrc(P.sa + c.m0, min(P.M - c.m0, (int64_t)BM) * 4), s + w * 256,
-               (w * 64 + lane) * 4, 0);
-      } else {
-        const int64_t nb = min(P.N - c.n0, (int64_t)BN) * 4;
-        dma<4>(make_rsrc(P.sb + c.n0, nb), s + 1024 + w * 256, (w * 64 + lane) * 4, 0);
-        dma<4>(P.bias ? make_rsrc(P.bias + c.n0, nb) : none, s + 2048 + w * 256, (w * 64 + lane) * 4, 0);
-      }
-    }
+    // Read after the last k-tile, several barriers later; the buffers
+    // alternate, so no wave still reads the one that is filled.
+    fetch_factors<BM, BN, 8>(reinterpret_cast<uint8_t*>(sc[turn]), P, c.m0, c.n0, none, wave, lane);
     for (int k = 0; k < np; k += 2) {
       ktile(st0, st1, c, n, has_next, none, O, F0, F1, acc, k, nk, np, wave);
       ktile(st1, st0, c, n, has_next, none, O, F0, F1, acc, k + 1, nk, np, wave);
     }
-    // acc[j][i] register 4 q + e: row arow0 + 32 i + 8 q + 4 half + e, column
-    // brow0 + 32 j + l32
-    const float* s = sc[turn];
-    float sb[TN], bias[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      sb[j] = s[256 + brow0 + 32 * j + l32];
-      bias[j] = s[512 + brow0 + 32 * j + l32];
-    }
-    const bool full = pairs && c.m0 + BM <= P.M && c.n0 + BN <= P.N;
-    constexpr int EB = OUT == kF32 ? 4 : 2;
-    const rsrc_t rc = make_rsrc(static_cast<uint8_t*>(P.C) + (c.m0 * P.ldc + c.n0) * EB, 256 * P.ldc * EB);
+    const float* f = sc[turn] + arow0;
+    const float* g = sc[turn] + 256 + brow0;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 sa4 = *reinterpret_cast<const float4*>(s + arow0 + 32 * i + 8 * q + 4 * half);
-        const float sa[4] = {sa4.x, sa4.y, sa4.z, sa4.w};
-        float v[TN][4];
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[j][e] = scaled(acc[j][i][4 * q + e], sa[e], sb[j], bias[j]);
-        if (!full) {
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int64_t m = c.m0 + arow0 + 32 * i + 8 * q + 4 * half + e;
-              const int64_t nn = c.n0 + brow0 + 32 * j + l32;
-              if (m < P.M && nn < P.N) put<OUT>(P.C, m * P.ldc + nn, v[j][e]);
-            }
-        } else if constexpr (OUT == kF32) {
-          // one register: two whole 128-byte row segments
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-              __builtin_amdgcn_raw_buffer_store_b32(
-                  __float_as_uint(v[j][e]), rc,
-                  (uint32_t)((arow0 + 4 * half) * P.ldc + brow0 + 32 * j + l32) * 4,
-                  (uint32_t)((32 * i + 8 * q + e) * P.ldc * 4), 2);
-        } else {
-          // Swapping halves of the two 32-column blocks gives a register 64
-          // consecutive columns of one row; two rows then trade values
-          // between neighbouring lanes: one 4-byte store holds two columns,
-          // even lanes of row R, odd lanes of row R + 1.
-          const int odd = lane & 1;
-          const uint32_t vb = (uint32_t)((arow0 + odd) * P.ldc + brow0 + lane - odd) * 2;
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const auto s0 = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[0][e]),
-                                                             __float_as_uint(v[1][e]), false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(
-                __float_as_uint(v[0][e + 1]), __float_as_uint(v[1][e + 1]), false, false);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // rows 8 q + e + 4 h and the next one
-              const uint32_t x = s0[h], y = s1[h];
-              const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? x : y), 0xb1, 0xf, 0xf, false);
-              const float lo = __uint_as_float(odd ? got : x), hi = __uint_as_float(odd ? y : got);
-              __builtin_amdgcn_raw_buffer_store_b32(
-                  pack2<OUT>(lo, hi), rc, vb, (uint32_t)((32 * i + 8 * q + e + 4 * h) * P.ldc * 2), 2);
-            }
-          }
-        }
-      }
+      put_pair<OUT>(acc[0][i], acc[1][i], staging + wave * kStage, Factors{f + 32 * i, g, g + 256}, P.C, P.ldc,
+                    c.m0 + arow0 + 32 * i, c.n0 + brow0, P.M, P.N, lane);
     if (!has_next) break;
     vt += step;
     c = n;
@@ -805,10 +904,7 @@ int cu_count() {
 template <int OUT>
 hipError_t launch(const Args& P, hipStream_t st) {
   const int64_t tiles = ((P.M + BM - 1) / BM) * ((P.N + BN - 1) / BN), ncu = cu_count();
-  // 4-byte stores of two 16-bit values need even pitches and a 4-byte base
-  const bool pairs = OUT == kF32 || (P.ldc % 2 == 0 && (uintptr_t)P.C % 4 == 0);
-  hipLaunchKernelGGL((gemm_kernel<OUT>), dim3((unsigned)(tiles < ncu ? tiles : ncu)), dim3(512), 0, st, P,
-                     pairs && P.ldc < (int64_t(1) << 22));
+  hipLaunchKernelGGL((gemm_kernel<OUT>), dim3((unsigned)(tiles < ncu ? tiles : ncu)), dim3(512), 0, st, P);
   return hipGetLastError();
 }
 
