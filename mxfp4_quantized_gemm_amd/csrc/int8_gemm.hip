@@ -930,24 +930,25 @@ struct Plan {
 };
 
 // The kernel and split with the least expected time, in us, by a model whose
-// constants were fitted to the times of all of them at 135 sizes (1 to 4096
-// tokens, weights of 155 x 1664 to 28672 x 4096): its choice is within 0.4% of
+// constants were fitted to the times of all of them at 197 sizes (1 to 4096
+// tokens, weights of 155 x 1664 to 28672 x 4096): its choice is within 0.3% of
 // the fastest on average, 10% at worst. Few tokens: a start, and for each
 // round of 256 work-groups and 1024 k a time that grows with M. Tiles: a start,
-// and for each round of 256 tiles c a k-tile, but no faster than B from memory,
-// the operands of all tiles through the caches, or the arithmetic; a split of
-// k adds a launch and its partial sums. Measured, for example, at 1024 x 4096
-// (N x K) and 64 tokens: few 10.8, 64 x 128 tiles 14.3, split in eight 8.6; at
-// 6144 x 4096 and 512 tokens 32.5 / 22.7 / 30.4 / 39.9 for the four tiles, and
-// at 1024 tokens 51.5 / 45.2 / 35.9 / 40.3.
+// and for each round of 256 tiles c a k-tile and an epilogue by the tile's
+// area, but no faster than B from memory, the operands of all tiles through
+// the caches, or the arithmetic; a split of k adds a launch and its partial
+// sums. Measured, for example, at 1024 x 4096 (N x K) and 64 tokens: few 10.8,
+// 64 x 128 tiles 12.4, split in eight 8.1; at 6144 x 4096 and 512 tokens 27.1 /
+// 19.8 / 25.7 / 40.5 for the four tiles, and at 1024 tokens 45.1 / 38.1 / 31.8 /
+// 40.7.
 float tiled_us(int64_t M, int64_t N, int64_t K, int bm, int bn, float c, int splits) {
   const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn), nk = K / KB;
   const int64_t rounds = (tiles * splits + 255) / 256;
-  float t = (float)(rounds * ((nk + splits - 1) / splits)) * c;
-  t = fmaxf(t, (float)N * K / 5.7e6f);
-  t = fmaxf(t, (float)(tiles * nk) * ((bm + bn) * KB) / 14e6f);
-  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 2.1e9f);
-  return 5.f + t + (splits > 1 ? 1.9f + (float)splits * M * N * 8.f / 2.7e6f : 0.f);
+  float t = (float)rounds * ((float)((nk + splits - 1) / splits) * c + 2.27f * (float)(bm * bn) / 65536.f);
+  t = fmaxf(t, (float)N * K / 7.9e6f);
+  t = fmaxf(t, (float)(tiles * nk) * ((bm + bn) * KB) / 17.3e6f);
+  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 3e9f);
+  return 2.7f + t + (splits > 1 ? 2.7f + (float)splits * M * N * 8.f / 3.9e6f : 0.f);
 }
 
 // Two groups of 16 rows of B to each load of A where that still gives most CUs
@@ -956,24 +957,29 @@ float tiled_us(int64_t M, int64_t N, int64_t K, int bm, int bn, float c, int spl
 bool two_groups(int64_t N) { return N > 4608; }
 
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  Plan best{k256x256, 1};
-  float t = tiled_us(M, N, K, 256, 256, 1.3f, 1);
+  Plan best{k64x128, 1};
+  float t = tiled_us(M, N, K, 64, 128, 0.3f, 1);
   const auto offer = [&](Kind kind, int splits, float us) {
     if (us < t) {
       t = us;
       best = {kind, splits};
     }
   };
-  for (int s : {1, 2, 3, 4, 6, 8}) {  // splits of at least 4 k-tiles
-    if (s > 1 && (s * 4 > K / KB || M > 4096)) break;  // (rows are a grid dimension of the sums)
-    if (s <= 2) offer(k128x256, s, tiled_us(M, N, K, 128, 256, 1.1f, s));
-    if (s <= 4) offer(k128x128, s, tiled_us(M, N, K, 128, 128, 0.77f, s));
-    offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.45f, s));
+  if (M > 64) {  // (larger tiles would be rows past the end)
+    offer(k128x128, 1, tiled_us(M, N, K, 128, 128, 0.445f, 1));
+    offer(k128x256, 1, tiled_us(M, N, K, 128, 256, 0.68f, 1));
+    offer(k256x256, 1, tiled_us(M, N, K, 256, 256, 0.725f, 1));
+  }
+  for (int s : {2, 3, 4, 6, 8}) {  // splits of at least 4 k-tiles
+    if (s * 4 > K / KB || M > 4096) break;  // (rows are a grid dimension of the sums)
+    offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.3f, s));
+    if (M > 64 && s <= 4) offer(k128x128, s, tiled_us(M, N, K, 128, 128, 0.445f, s));
+    if (M > 64 && s <= 2) offer(k128x256, s, tiled_us(M, N, K, 128, 256, 0.68f, s));
   }
   if (M <= 64) {
     const int64_t rows = two_groups(N) ? 8192 : 4096;  // 256 work-groups' rows of B
-    const float per = (0.59f + 0.027f * M) * (two_groups(N) ? 1.7f : 1.f);
-    offer(kFew, 1, 2.8f + fmaxf((float)((N + rows - 1) / rows) * K / 1024.f * per, (float)N * K / 5.7e6f));
+    const float per = (0.326f + 0.0246f * M) * (!two_groups(N) ? 1.f : M <= 16 && K <= 1024 ? 1.2f : 1.56f);
+    offer(kFew, 1, 2.8f + fmaxf((float)((N + rows - 1) / rows) * K / 1024.f * per, (float)N * K / 7.9e6f));
   }
   return best;
 }
@@ -984,6 +990,8 @@ hipError_t launch_out(const Args& P, void* ws, hipStream_t st) {
   const Plan plan = plan_of(P.M, P.N, P.K);
   switch (plan.kind) {
     case kFew:
+      // few chunks of k leave 8 waves half idle (22741 x 512, M = 1: 4.4 against 5.2)
+      if (P.M <= 16 && two_groups(P.N) && P.K <= 1024) return few::launch<4, 4, 1, 2, OUT>(P, st);
       if (P.M <= 16)
         return two_groups(P.N) ? few::launch<8, 4, 1, 2, OUT>(P, st) : few::launch<8, 4, 1, 1, OUT>(P, st);
       if (P.M <= 32)
