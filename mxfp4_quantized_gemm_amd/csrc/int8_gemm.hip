@@ -670,14 +670,28 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
     }
 }
 
+// Four columns a thread, at any alignment.
 template <int OUT>
 __global__ __launch_bounds__(256) void sum_kernel(Args P, int splits, const int* part) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
+  typedef v4i v4i_4 __attribute__((aligned(4)));
+  const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, m = blockIdx.y;
   if (n >= P.N) return;
-  int s = 0;
+  const float sa = P.sa[m];
+  const int* p = part + m * P.N + n;
+  if (n + 4 <= P.N) {
+    v4i s = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int z = 0; z < splits; ++z) s += part[((int64_t)z * P.M + m) * P.N + n];
-  put<OUT>(P.C, m * P.ldc + n, scaled(s, P.sa[m], P.sb[n], P.bias ? P.bias[n] : 0.f));
+    for (int z = 0; z < splits; ++z) s += *reinterpret_cast<const v4i_4*>(p + z * P.M * P.N);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      put<OUT>(P.C, m * P.ldc + n + e, scaled(s[e], sa, P.sb[n + e], P.bias ? P.bias[n + e] : 0.f));
+  } else {
+    for (int e = 0; n + e < P.N; ++e) {
+      int s = 0;
+      for (int z = 0; z < splits; ++z) s += p[z * P.M * P.N + e];
+      put<OUT>(P.C, m * P.ldc + n + e, scaled(s, sa, P.sb[n + e], P.bias ? P.bias[n + e] : 0.f));
+    }
+  }
 }
 
 template <class T, int OUT>
@@ -688,7 +702,7 @@ hipError_t launch(const Args& P, int splits, void* ws, hipStream_t st) {
   if (splits > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((sum_kernel<OUT>), dim3((unsigned)((P.N + 255) / 256), (unsigned)P.M), dim3(256), 0,
+    hipLaunchKernelGGL((sum_kernel<OUT>), dim3((unsigned)((P.N + 1023) / 1024), (unsigned)P.M), dim3(256), 0,
                        st, P, splits, static_cast<const int*>(ws));
   }
   return hipGetLastError();
