@@ -315,3 +315,111 @@ def test_graph_replays(T):
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(out, want)), i
         torch.randn(1000, device="cuda").sum()
+
+
+# --------------------------------------- offsets past 32 bits, C-named calls
+def sampled(c, a, b, sa, sb, rows, cols):
+    """Rows and columns of C against fp64 sums of the same codes."""
+    s = a[rows].double() @ b[cols].double().t()
+    p = s * sa[rows].double()[:, None] * sb[cols].double()
+    tol = p.abs() * (4 * U + torch.finfo(c.dtype).eps / 2) + 1e-30
+    got = c[rows][:, cols].double()
+    assert ((got - p).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(70000, 96, 65536), (3, 70000, 65536), (48, 70000, 65536), (40000, 60000, 128),
+                                   (70000, 200, 65504)],
+                         ids=["A over 4 GiB", "B over 4 GiB, few", "B over 4 GiB", "C over 4 GiB", "A over 4 GiB, general"])
+def test_product_past_32_bits(M, N, K):
+    from mxfp4_quantized_gemm_amd.int8 import int8_gemm
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    a = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    b = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    sa, sb = torch.rand(M, device="cuda", generator=g) + 0.1, torch.rand(N, device="cuda", generator=g) + 0.1
+    c = int8_gemm(a, sa, b, sb)
+    pick = lambda n: torch.tensor(sorted({0, 1, n // 3, n // 2, n - 2, n - 1} & set(range(n))), device="cuda")
+    sampled(c, a, b, sa, sb, pick(M), pick(N))
+    del a, b, c
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("cols", [32768, 32767])
+def test_rows_past_32_bits(cols):
+    """70000 rows: over 4 GiB of bf16, both sides of every 32-bit border."""
+    from mxfp4_quantized_gemm_amd.int8 import int8_quantize
+    from mxfp4_quantized_gemm_amd.norm import rms_norm_int8
+    rows = 70000
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[:] = torch.arange(-2, cols - 2, device="cuda") % 97 - 48.0
+    x *= (torch.arange(rows, device="cuda") % 31 + 1.0)[:, None]
+    at = [0, 1, 32767, 32768, 65535, 65536, 65538, rows - 1]
+    codes, scales = int8_quantize(x)
+    check_codes(codes[at], scales[at], x[at].float().cpu().numpy())
+    codes, scales = rms_norm_int8(x, None, EPS)
+    h = x[at].cpu()
+    r = (1 / torch.sqrt(h.double().square().sum(1, keepdim=True) / cols + float(F(EPS)))).float()
+    check_codes(codes[at], scales[at], (h.float() * r).numpy())
+    del x, codes
+    torch.cuda.empty_cache()
+
+
+def test_c_named_calls_on_a_stream():
+    """The ctypes binding, with the caller's buffers and stream, gives the
+    bits of the functions that allocate."""
+    import mxfp4_quantized_gemm_amd as mx
+    from mxfp4_quantized_gemm_amd import int8, norm
+    T, K, N = 70, 333, 96
+    x, res, dy, dh = (rand((T, K), torch.bfloat16, i).cuda() for i in range(4))
+    w = rand((K,), torch.bfloat16, 5).cuda()
+    wq, ws = int8.int8_quantize(rand((N, K), torch.bfloat16, 6).cuda())
+    q, s, h = norm.rms_norm_int8(x, w, EPS, residual=res)
+    c = int8.int8_gemm(q, s, wq, ws)
+    g, gs = int8.int8_quantize(x, gate=res)
+    leaves = [t.clone().requires_grad_(True) for t in (x, res, w)]
+    y, _ = out = norm.rms_norm(leaves[0], leaves[2], EPS, residual=leaves[1])
+    dx, _, dw = torch.autograd.grad(out, leaves, (dy, dh))
+    torch.cuda.synchronize()
+
+    st = torch.cuda.Stream()
+    new = lambda *shape, dtype=torch.bfloat16: torch.empty(*shape, dtype=dtype, device="cuda")
+    h2, y2, dx2, dw2, rstd = new(T, K), new(T, K), new(T, K), new(K), new(T, dtype=torch.float32)
+    q2, s2 = new(T, 384, dtype=torch.int8), new(T, dtype=torch.float32)
+    g2, gs2 = new(T, 384, dtype=torch.int8), new(T, dtype=torch.float32)
+    c2 = new(T, N)
+    need = mx.mxfp4_int8_gemm_workspace_bytes(T, N, 384)
+    gemm_ws = new(need, dtype=torch.uint8) if need else None
+    bwd_ws = new(mx.mxfp4_rmsnorm_bwd_workspace_bytes(T, K), dtype=torch.uint8)
+    torch.cuda.synchronize()
+    mx.mxfp4_rmsnorm_int8(x, res, w, EPS, h2, q2, s2, stream=st)
+    mx.mxfp4_int8_gemm(q2, s2, wq, ws, None, c2, gemm_ws, stream=st)
+    mx.mxfp4_int8_quantize(x, res, g2, gs2, stream=st)
+    mx.mxfp4_rmsnorm(x, res, w, EPS, None, y2, rstd, stream=st)
+    mx.mxfp4_rmsnorm_bwd(dy, dh, h2, w, rstd, dx2, dw2, bwd_ws, stream=st.cuda_stream)
+    st.synchronize()
+    for a, b in ((h, h2), (q, q2), (s, s2), (c, c2), (g, g2), (gs, gs2), (y, y2), (dx, dx2), (dw, dw2)):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        mx.mxfp4_rmsnorm(x, res, w, EPS, None, y2[:3], rstd)
+    with pytest.raises(TypeError):
+        mx.mxfp4_rmsnorm(x, res.float(), w, EPS, None, y2, rstd)
+    with pytest.raises(ValueError):
+        mx.mxfp4_int8_gemm(q2.t(), s2, wq, ws, None, c2, None)
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 100, 4096), (200, 130, 2048), (33, 4099, 1024), (300, 1000, 8192)])
+def test_product_without_its_workspace_is_refused(M, N, K):
+    import mxfp4_quantized_gemm_amd as mx
+    need = mx.mxfp4_int8_gemm_workspace_bytes(M, N, K)
+    a, b = torch.zeros(M, K, dtype=torch.int8, device="cuda"), torch.zeros(N, K, dtype=torch.int8, device="cuda")
+    sa, sb = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    c = torch.empty(M, N, device="cuda")
+    if need:
+        with pytest.raises(mx.MXFP4Error) as e:
+            mx.mxfp4_int8_gemm(a, sa, b, sb, None, c, None)
+        assert e.value.status == 1
+        with pytest.raises(mx.MXFP4Error) as e:
+            mx.mxfp4_int8_gemm(a, sa, b, sb, None, c, torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
+        assert e.value.status == 4
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    mx.mxfp4_int8_gemm(a, sa, b, sb, None, c, ws)
+    assert not c.any()
