@@ -284,12 +284,11 @@ def test_mlp_block():
     assert y3.shape == (1, T, K) and h3.shape == (1, T, K)
 
 
-@pytest.mark.parametrize("T", [2, 48, 512])
-def test_graph_replays(T):
+@pytest.mark.parametrize("T,K,N", [(2, 1024, 768), (48, 1024, 768), (512, 1024, 768), (65, 4096, 4100), (2100, 512, 2100)])
+def test_graph_replays(T, K, N):
     """Decode's sequence in a HIP graph: every replay equals the eager result,
     with the inputs overwritten and other work in between."""
     from mxfp4_quantized_gemm_amd import int8, norm
-    K, N = 1024, 768
     x, res = rand((T, K), torch.bfloat16, 0).cuda(), rand((T, K), torch.bfloat16, 1).cuda()
     w = rand((K,), torch.bfloat16, 2).cuda()
     b, sb = int8.int8_quantize(rand((N, K), torch.bfloat16, 3).cuda())
@@ -423,3 +422,18 @@ def test_product_without_its_workspace_is_refused(M, N, K):
     ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
     mx.mxfp4_int8_gemm(a, sa, b, sb, None, c, ws)
     assert not c.any()
+
+
+# Sizes past those above, so that every tile, split and streaming form is
+# reached: several rounds of tiles, one and an odd number of k-tiles, ragged
+# edges in both directions.
+LARGER = [(1, 5003, 384), (5, 5000, 2048), (9, 12010, 384), (16, 6144, 1408), (20, 5001, 640), (40, 5003, 256),
+          (64, 8200, 128), (64, 28672, 256), (129, 14336, 384), (200, 4100, 8192), (60, 8200, 8192), (65, 8000, 8192), (65, 14000, 14336), (130, 14000, 14336), (400, 2050, 8192),
+          (512, 4100, 2048), (520, 8190, 640), (640, 14337, 256), (1300, 2100, 512), (2301, 3503, 640), (3000, 3000, 384),
+          (5001, 5100, 128), (4097, 4097, 256)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", LARGER, ids=lambda s: "x".join(map(str, s)))
+def test_larger_product(size, dtype):
+    product(*size, TYPES[dtype], seed=sum(size), bias=dtype == "bf16")
