@@ -87,8 +87,8 @@ template <int OUT>
 __global__ __launch_bounds__(256) void gemm_kernel(Args P, bool vec) {
   __shared__ __attribute__((aligned(16))) uint8_t la[BM * PITCH], lb[BN * PITCH];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int64_t ntn = (P.N + BN - 1) / BN;
-  const int64_t m0 = blockIdx.x / ntn * BM, n0 = blockIdx.x % ntn * BN;
+  const uint32_t ntn = (uint32_t)((P.N + BN - 1) / BN), tm = blockIdx.x / ntn;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)(blockIdx.x - tm * ntn) * BN;
   const int wm = wave >> 1, wn = wave & 1;
   const int r = t >> 2, c = (t & 3) * 16;  // the thread's chunk of a tile
   const uint8_t* fa = la + (wm * 32 + (lane & 31)) * PITCH + (lane >> 5) * 16;
@@ -187,16 +187,17 @@ __device__ __forceinline__ uint32_t frag_off(int s, int lane) {
 // Work-group id -> output tile. Consecutive ids go round-robin over the 8
 // XCDs; each XCD gets a contiguous range of logical tiles, walked in groups
 // of 4 tile-rows, so that the tiles resident on one XCD share operand rows in
-// its L2.
-__device__ __forceinline__ void tile_of(int64_t wg, int64_t nwg, int64_t ntm, int64_t ntn,
-                                        int64_t& tm, int64_t& tn) {
-  const int64_t per = nwg / 8;
-  int64_t lg = wg;
+// its L2. (There are at most 2^23 tiles. Divisions of 64 bits cost 1 us before the
+// first load: 64 x 1024 x 1024 6.0 -> 5.0, 333 x 1537 x 2816 11.5 -> 10.1.)
+__device__ __forceinline__ void tile_of(uint32_t wg, uint32_t nwg, uint32_t ntm, uint32_t ntn,
+                                        uint32_t& tm, uint32_t& tn) {
+  const uint32_t per = nwg / 8;
+  uint32_t lg = wg;
   if (wg < per * 8) lg = (wg % 8) * per + wg / 8;
-  const int64_t width = 4 * ntn, g = lg / width, first = g * 4;
-  const int64_t gs = min(ntm - first, (int64_t)4), r = lg % width;
-  tm = first + r % gs;
+  const uint32_t width = 4 * ntn, g = lg / width, first = g * 4;
+  const uint32_t gs = min(ntm - first, 4u), r = lg - g * width;
   tn = r / gs;
+  tm = first + r - tn * gs;
 }
 
 // ------------------------------------------------------------- epilogue
@@ -399,9 +400,14 @@ __global__ __launch_bounds__(64 * W) void gemm_kernel(Args P) {
   for (int h = 0; h < NG; ++h)
 #pragma unroll
     for (int g = 0; g < MG; ++g) acc[h][g] = v4i{0, 0, 0, 0};
+  // Work-groups start at different chunks and wrap around: rows whose pitch is
+  // a multiple of 4 KiB would else be read at the same place of it by all of
+  // them, which is the same few memory channels (one token, us: 8192 x 8192
+  // 17.2 -> 11.7, 4096 x 4096 5.4 -> 4.7, 4096 x 14336 as before).
+  const int rot = (int)(blockIdx.x / 8 * 4 % (unsigned)chunks);
   auto load = [&](int u, int c) {
     const uint32_t dead = c < chunks ? 0u : 0x80000000u;  // rows are below 2^23 bytes
-    const uint32_t so = (uint32_t)c * 64;
+    const uint32_t so = (uint32_t)(c + rot - (c + rot >= chunks ? chunks : 0)) * 64;
 #pragma unroll
     for (int h = 0; h < NG; ++h)
       qb[u][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rb, vb[h] | dead, so, 0));
@@ -409,8 +415,11 @@ __global__ __launch_bounds__(64 * W) void gemm_kernel(Args P) {
     for (int g = 0; g < MG; ++g)
       qa[u][g] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(ra, va[g] | dead, so, 0));
   };
+  // a wave's loads take the two halves of 128-byte lines one after the other
+  static_assert(U % 2 == 0, "pairs of chunks");
+  auto chunk = [&](int u) { return 2 * wave + u / 2 * 2 * W + u % 2; };
 #pragma unroll
-  for (int u = 0; u < U; ++u) load(u, wave + W * u);
+  for (int u = 0; u < U; ++u) load(u, chunk(u));
   auto mul = [&](int u) {
 #pragma unroll
     for (int h = 0; h < NG; ++h)
@@ -422,7 +431,7 @@ __global__ __launch_bounds__(64 * W) void gemm_kernel(Args P) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       mul(u);
-      load(u, c + wave + W * u);
+      load(u, c + chunk(u));
     }
   }
 #pragma unroll
@@ -554,13 +563,21 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / T::WN, wn = wave % T::WN;
-  const int64_t ntm = (P.M + T::BM - 1) / T::BM, ntn = (P.N + T::BN - 1) / T::BN;
-  int64_t tm, tn;
+  const uint32_t ntm = (uint32_t)((P.M + T::BM - 1) / T::BM), ntn = (uint32_t)((P.N + T::BN - 1) / T::BN);
+  uint32_t tm, tn;
   tile_of(blockIdx.x, gridDim.x, ntm, ntn, tm, tn);
-  const int64_t m0 = tm * T::BM, n0 = tn * T::BN;
+  const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
   // the split's k-tiles: [k0, k0 + nk), at least one
   const int all = (int)(P.K / KB), z = blockIdx.y;
-  const int k0 = (int)((int64_t)all * z / splits), nk = (int)((int64_t)all * (z + 1) / splits) - k0;
+  const int k0 = all * z / splits, nk = all * (z + 1) / splits - k0;
+  // Tiles start at different k-tiles and wrap around, where B streams from
+  // memory: rows whose pitch is a multiple of 4 KiB would else be read at the
+  // same place of that pitch by all tiles at once, which is the same few memory
+  // channels (28672 x 4096, us: 16 tokens 25.4 -> 21.7, 64 tokens 26.8 -> 23.6;
+  // 28672 x 8192 48.5 -> 37.9). Other tiles share A's rows in the L2 by running
+  // in step (512 x 6144 x 4096: 19.5, rotated 21.1).
+  const int rot = T::NTB ? (int)(tn * (uint32_t)nk / ntn) : 0;
+  auto at = [&](int k) { return (uint32_t)(k0 + k + rot - (k + rot >= nk ? nk : 0)) * KB; };
   const rsrc_t ra = rows_rsrc(P.A, m0, P.M, T::BM, P.lda), rb = rows_rsrc(P.B, n0, P.N, T::BN, P.ldb);
   const rsrc_t none = make_rsrc(P.A, 0);
   Lane<T> L;
@@ -588,8 +605,8 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
   if (splits == 1) fetch_factors<T::BM, T::BN, T::NW>(factors, P, m0, n0, none, wave, lane);
 #pragma unroll
   for (int k = 0; k < NS - 1; ++k)
-    fetch<T>(slot(k), ra, rb, none, k < nk, L, (uint32_t)(k0 + k) * KB, wave);
-  fetch<T, 0, NB / T::SP>(slot(NS - 1), ra, rb, none, NS - 1 < nk, L, (uint32_t)(k0 + NS - 1) * KB, wave);
+    fetch<T>(slot(k), ra, rb, none, k < nk, L, at(k), wave);
+  fetch<T, 0, NB / T::SP>(slot(NS - 1), ra, rb, none, NS - 1 < nk, L, at(NS - 1), wave);
   wait_vm<(NS - 2) * NB + NB / T::SP>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -606,7 +623,7 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
   auto part_of = [&](auto S, auto Q, int k) {  // part Q of k-tile k into slot S
     constexpr int u0 = NB * Q.value / T::SP, u1 = NB * (Q.value + 1) / T::SP;
     if constexpr (Q.value < T::SP)
-      fetch<T, u0, u1>(slot(S.value), ra, rb, none, k < nk, L, (uint32_t)(k0 + k) * KB, wave);
+      fetch<T, u0, u1>(slot(S.value), ra, rb, none, k < nk, L, at(k), wave);
   };
   auto count = [](int q) { return q < T::SP ? NB * (q + 1) / T::SP - NB * q / T::SP : 0; };
   auto step = [&](auto S, int k) {
@@ -837,13 +854,13 @@ __device__ __forceinline__ void ktile(uint8_t* st, uint8_t* nx, const Tile& c, c
   __builtin_amdgcn_sched_barrier(0);
 }
 
-__device__ __forceinline__ Tile tile_at(const Args& P, int64_t vt, int64_t ntiles, int64_t ntm,
-                                        int64_t ntn) {
+__device__ __forceinline__ Tile tile_at(const Args& P, uint32_t vt, uint32_t ntiles, uint32_t ntm,
+                                        uint32_t ntn) {
   Tile T;
-  int64_t tm, tn;
+  uint32_t tm, tn;
   tile_of(vt, ntiles, ntm, ntn, tm, tn);
-  T.m0 = tm * BM;
-  T.n0 = tn * BN;
+  T.m0 = (int64_t)tm * BM;
+  T.n0 = (int64_t)tn * BN;
   T.a = rows_rsrc(P.A, T.m0, P.M, BM, P.lda);
   T.b = rows_rsrc(P.B, T.n0, P.N, BN, P.ldb);
   return T;
@@ -859,8 +876,8 @@ void gemm_kernel(Args P) {
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int64_t ntm = (P.M + BM - 1) / BM, ntn = (P.N + BN - 1) / BN, ntiles = ntm * ntn;
-  const int64_t step = gridDim.x;
+  const uint32_t ntm = (uint32_t)((P.M + BM - 1) / BM), ntn = (uint32_t)((P.N + BN - 1) / BN);
+  const uint32_t ntiles = ntm * ntn, step = gridDim.x;
   const int nk = (int)(P.K / KB), np = (nk + 1) & ~1;
   const int arow0 = wm * TM * 32, brow0 = wn * TN * 32;
   const rsrc_t none = make_rsrc(P.A, 0);
@@ -875,7 +892,7 @@ void gemm_kernel(Args P) {
     O.fa[s] = (uint32_t)(arow0 * KB) + frag_off(s, lane);
     O.fb[s] = (uint32_t)(TILE + brow0 * KB) + frag_off(s, lane);
   }
-  int64_t vt = blockIdx.x;
+  uint32_t vt = blockIdx.x;
   Tile c = tile_at(P, vt, ntiles, ntm, ntn);
   bool has_next = vt + step < ntiles;
   Tile n = has_next ? tile_at(P, vt + step, ntiles, ntm, ntn) : c;
