@@ -474,7 +474,7 @@ hipError_t launch(const Args& P, hipStream_t st) {
 // ring, with the operands in L2 or not), so a tile wants many waves: 128 x 128
 // takes 0.37 us a k-tile with 16 waves of 32 x 32, 0.40 with 8 of 64 x 32 and
 // 0.53 with 4 of 64 x 64, against 0.21 of MFMA work. For few tokens it is B
-// from memory: 28672 x 4096, 64 tokens in 26.4 us, 4.6 TB/s.
+// from memory: 28672 x 4096, 64 tokens in 22.5 us, 5.4 TB/s.
 namespace ring {
 
 template <int WM_, int WN_, int TM_, int TN_, int NS_, int SP_ = 4, int NTB_ = 0>
@@ -981,36 +981,39 @@ struct Plan {
   int splits;
 };
 
+// From this size on a weight is counted as coming from HBM each time.
+constexpr int64_t kPastCache = int64_t(1) << 27;
+
 // The kernel and split with the least expected time, in us, by a model whose
-// constants were fitted to the times of all of them at 197 sizes (1 to 4096
-// tokens, weights of 155 x 1664 to 28672 x 4096): its choice is within 0.3% of
-// the fastest on average, 10% at worst. Few tokens: a start, and for each
+// constants were fitted to the times of all of them at 189 sizes (1 to 4096
+// tokens, weights of 128 x 384 to 28672 x 4096): its choice is within 0.7% of
+// the fastest on average, 23% at worst. Few tokens: a start, and for each
 // round of 256 work-groups and 1024 k a time that grows with M. Tiles: a start,
 // and for each round of 256 tiles c a k-tile and an epilogue by the tile's
 // area, but no faster than B from memory, the operands of all tiles through
 // the caches, or the arithmetic; a split of k adds a launch and its partial
-// sums. Measured, for example, at 1024 x 4096 (N x K) and 64 tokens: few 10.8,
-// 64 x 128 tiles 12.4, split in eight 8.1; at 6144 x 4096 and 512 tokens 27.1 /
-// 19.8 / 25.7 / 40.5 for the four tiles, and at 1024 tokens 45.1 / 38.1 / 31.8 /
-// 40.7.
+// sums. Measured, for example, at 1024 x 4096 (N x K) and 64 tokens: few 11.0,
+// 64 x 128 tiles 9.4, split in eight 8.6; at 6144 x 4096 and 512 tokens 25.8 /
+// 18.0 / 23.7 / 40.0 for the four tiles, and at 1024 tokens 39.4 / 35.0 / 28.1 /
+// 40.3.
 float tiled_us(int64_t M, int64_t N, int64_t K, int bm, int bn, float c, int splits) {
   const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn), nk = K / KB;
   const int64_t rounds = (tiles * splits + 255) / 256;
-  float t = (float)rounds * ((float)((nk + splits - 1) / splits) * c + 2.27f * (float)(bm * bn) / 65536.f);
-  t = fmaxf(t, (float)N * K / 7.9e6f);
-  t = fmaxf(t, (float)(tiles * nk) * ((bm + bn) * KB) / 17.3e6f);
-  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 3e9f);
-  return 2.7f + t + (splits > 1 ? 2.7f + (float)splits * M * N * 8.f / 3.9e6f : 0.f);
+  float t = (float)rounds * ((float)((nk + splits - 1) / splits) * c + 4.35f * (float)(bm * bn) / 65536.f);
+  t = fmaxf(t, (float)N * K / (N * K >= kPastCache ? 6.31e6f : 8e6f));
+  t = fmaxf(t, (float)(tiles * nk) * ((bm + bn) * KB) / 13.1e6f);
+  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 2.33e9f);
+  return 2.17f + t + (splits > 1 ? 3.58f + (float)splits * M * N * 8.f / 3.19e6f : 0.f);
 }
 
 // Two groups of 16 rows of B to each load of A where that still gives most CUs
-// a work-group (us, one group / two: 6144 x 4096, M = 4 8.8 / 6.9, M = 16 10.2 /
-// 7.9, M = 64 20.0 / 14.0; 1024 x 4096, M = 16 5.4 / 7.4).
+// a work-group (us, one group / two: 6144 x 4096, M = 4 7.5 / 7.0, M = 16 9.4 /
+// 8.1, M = 64 20.3 / 14.3; 1024 x 4096, M = 16 5.4 / 7.4).
 bool two_groups(int64_t N) { return N > 4608; }
 
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   Plan best{k64x128, 1};
-  float t = tiled_us(M, N, K, 64, 128, 0.3f, 1);
+  float t = tiled_us(M, N, K, 64, 128, 0.347f, 1);
   const auto offer = [&](Kind kind, int splits, float us) {
     if (us < t) {
       t = us;
@@ -1018,20 +1021,21 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
     }
   };
   if (M > 64) {  // (larger tiles would be rows past the end)
-    offer(k128x128, 1, tiled_us(M, N, K, 128, 128, 0.445f, 1));
-    offer(k128x256, 1, tiled_us(M, N, K, 128, 256, 0.68f, 1));
-    offer(k256x256, 1, tiled_us(M, N, K, 256, 256, 0.725f, 1));
+    offer(k128x128, 1, tiled_us(M, N, K, 128, 128, 0.462f, 1));
+    offer(k128x256, 1, tiled_us(M, N, K, 128, 256, 0.732f, 1));
+    offer(k256x256, 1, tiled_us(M, N, K, 256, 256, 1.01f, 1));
   }
   for (int s : {2, 3, 4, 6, 8}) {  // splits of at least 4 k-tiles
     if (s * 4 > K / KB || M > 4096) break;  // (rows are a grid dimension of the sums)
-    offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.3f, s));
-    if (M > 64 && s <= 4) offer(k128x128, s, tiled_us(M, N, K, 128, 128, 0.445f, s));
-    if (M > 64 && s <= 2) offer(k128x256, s, tiled_us(M, N, K, 128, 256, 0.68f, s));
+    offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.347f, s));
+    if (M > 64 && s <= 4) offer(k128x128, s, tiled_us(M, N, K, 128, 128, 0.462f, s));
+    if (M > 64 && s <= 2) offer(k128x256, s, tiled_us(M, N, K, 128, 256, 0.732f, s));
   }
   if (M <= 64) {
     const int64_t rows = two_groups(N) ? 8192 : 4096;  // 256 work-groups' rows of B
-    const float per = (0.326f + 0.0246f * M) * (!two_groups(N) ? 1.f : M <= 16 && K <= 1024 ? 1.2f : 1.56f);
-    offer(kFew, 1, 2.8f + fmaxf((float)((N + rows - 1) / rows) * K / 1024.f * per, (float)N * K / 7.9e6f));
+    const float per = (0.426f + 0.0291f * M) * (!two_groups(N) ? 1.f : M <= 16 && K <= 1024 ? 1.72f : 1.39f);
+    const float mem = (float)N * K / (N * K >= kPastCache ? 4.45e6f : 6.15e6f);
+    offer(kFew, 1, 2.58f + fmaxf((float)((N + rows - 1) / rows) * K / 1024.f * per, mem));
   }
   return best;
 }
@@ -1051,9 +1055,9 @@ hipError_t launch_out(const Args& P, void* ws, hipStream_t st) {
       return two_groups(P.N) ? few::launch<4, 4, 4, 2, OUT>(P, st) : few::launch<8, 2, 4, 1, OUT>(P, st);
     case k64x128:
       // One tile-row reads B once. A large weight comes from HBM each time, and
-      // past the caches is faster (28672 x 4096, M = 64: 29.0 against 33.9 us);
+      // past the caches is faster (28672 x 4096, M = 64: 23.8 against 28.3 us);
       // a smaller one may still lie in the 256 MB cache (6144 x 4096, used
-      // again after two others of its size: 15.9 kept against 21.0).
+      // again after two others of its size: 12.2 kept against 17.0).
       if (P.M <= 64 && P.N * P.K >= (int64_t(1) << 26))
         return ring::launch<R64x128nt, OUT>(P, plan.splits, ws, st);
       return ring::launch<R64x128, OUT>(P, plan.splits, ws, st);
