@@ -469,12 +469,15 @@ hipError_t launch(const Args& P, hipStream_t st) {
 // are fewer output tiles than CUs the k range is split over blockIdx.y: the
 // int32 partial sums go to the workspace and a second kernel adds them (the
 // sums are exact, so the split does not show in the result).
-// What bounds it: a wave waits at its DMAs and LDS reads while its MFMAs are
-// done (8 reads and 4 DMAs about 330 clocks a k-tile, whatever the depth of the
-// ring, with the operands in L2 or not), so a tile wants many waves: 128 x 128
-// takes 0.37 us a k-tile with 16 waves of 32 x 32, 0.40 with 8 of 64 x 32 and
-// 0.53 with 4 of 64 x 64, against 0.21 of MFMA work. For few tokens it is B
-// from memory: 28672 x 4096, 64 tokens in 22.5 us, 5.4 TB/s.
+// What bounds it: the LDS, written by DMA at 64 bytes a clock and read at 256,
+// not both at once. A k-tile of 64 x 128 (8 waves of 32 x 32) is 384 + 256
+// clocks and takes 0.26 us whether a third of the CUs work or all, beside 256
+// clocks of MFMAs; 128 x 128 with 8 waves of 64 x 32 is 512 + 384 (16 waves of
+// 32 x 32: 512 + 512; 512 x 6144 x 4096 16.6 against 17.4 us), 128 x 256 with 8
+// waves of 64 x 64 is 768 + 512 (16 of 32 x 64: 768 + 768; 1024 x 6144 x 4096
+// 27.1 against 28.0). Fragments read a whole k-tile ahead, and rows touched in
+// the L2 up to 16 k-tiles ahead by a wave of its own, gained nothing. For few
+// tokens it is B from memory: 28672 x 4096, 64 tokens in 21.2 us, 5.7 TB/s.
 namespace ring {
 
 template <int WM_, int WN_, int TM_, int TN_, int NS_, int SP_ = 4, int NTB_ = 0>
@@ -548,6 +551,16 @@ __device__ __forceinline__ void interleave() {
     interleave<T, R + 1, NL>();
   } else {
     __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Steps k, k + 1, ... (at most N) that lie below end.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void steps(F& step, int k, int end) {
+  if constexpr (I < N) {
+    if (k + I >= end) return;
+    step(std::integral_constant<int, I>{}, k + I);
+    steps<N, I + 1>(step, k, end);
   }
 }
 
@@ -650,30 +663,13 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
     mul<T>(F1, acc);
     interleave<T, 0, count(0)>();
   };
-  // Only a whole turn of the ring reaches the loop's back edge: the compiler
-  // would else see a path on which slot 0 was just fetched, and wait for it.
-  for (int k = 0;; k += NS) {
-    step(std::integral_constant<int, 0>{}, k);
-    if (k + 1 >= nk) break;
-    step(std::integral_constant<int, 1>{}, k + 1);
-    if (k + 2 >= nk) break;
-    if constexpr (NS > 2) {
-      step(std::integral_constant<int, 2>{}, k + 2);
-      if (k + 3 >= nk) break;
-    }
-    if constexpr (NS > 3) {
-      step(std::integral_constant<int, 3>{}, k + 3);
-      if (k + 4 >= nk) break;
-    }
-    if constexpr (NS > 4) {
-      step(std::integral_constant<int, 4>{}, k + 4);
-      if (k + 5 >= nk) break;
-    }
-    if constexpr (NS > 5) {
-      step(std::integral_constant<int, 5>{}, k + 5);
-      if (k + 6 >= nk) break;
-    }
-  }
+  // Whole turns of the ring, then the rest: with exits inside the loop the
+  // compiler saw ways to its start on which slot 0 was just fetched, and waited
+  // there for all DMAs (512 x 6144 x 4096 18.7 -> 17.4, 64 x 28672 x 4096
+  // 22.7 -> 21.2).
+  int k = 0;
+  for (; k + NS <= nk; k += NS) steps<NS>(step, k, k + NS);
+  steps<NS - 1>(step, k, nk);
   // The last (empty) DMAs land and every wave is done with the slots: the
   // first ones become the waves' staging of the epilogue.
   wait_vm<0, true>();
@@ -971,8 +967,8 @@ bool fast_ok(const Args& P) {
 // ----------------------------------------------------------- choice
 typedef ring::G<2, 4, 1, 1, 6, 3> R64x128;
 typedef ring::G<2, 4, 1, 1, 6, 3, 1> R64x128nt;
-typedef ring::G<4, 4, 1, 1, 4, 2> R128x128;
-typedef ring::G<4, 4, 1, 2, 3, 3> R128x256;
+typedef ring::G<2, 4, 2, 1, 4, 4> R128x128;
+typedef ring::G<2, 4, 2, 2, 3, 3> R128x256;
 
 enum Kind { kFew, k64x128, k128x128, k128x256, k256x256 };
 
@@ -986,16 +982,16 @@ constexpr int64_t kPastCache = int64_t(1) << 27;
 
 // The kernel and split with the least expected time, in us, by a model whose
 // constants were fitted to the times of all of them at 189 sizes (1 to 4096
-// tokens, weights of 128 x 384 to 28672 x 4096): its choice is within 0.7% of
-// the fastest on average, 23% at worst. Few tokens: a start, and for each
+// tokens, weights of 128 x 384 to 28672 x 4096): its choice is within 0.8% of
+// the fastest on average, 26% at worst (1440 x 3551 x 384, where C's bytes rule). Few tokens: a start, and for each
 // round of 256 work-groups and 1024 k a time that grows with M. Tiles: a start,
 // and for each round of 256 tiles c a k-tile and an epilogue by the tile's
 // area, but no faster than B from memory, the operands of all tiles through
 // the caches, or the arithmetic; a split of k adds a launch and its partial
 // sums. Measured, for example, at 1024 x 4096 (N x K) and 64 tokens: few 11.0,
-// 64 x 128 tiles 9.4, split in eight 8.6; at 6144 x 4096 and 512 tokens 25.8 /
-// 18.0 / 23.7 / 40.0 for the four tiles, and at 1024 tokens 39.4 / 35.0 / 28.1 /
-// 40.3.
+// 64 x 128 tiles 8.8, split in eight 8.1; at 6144 x 4096 and 512 tokens 22.8 /
+// 16.3 / 22.8 / 39.9 for the four tiles, and at 1024 tokens 39.0 / 32.7 / 27.2 /
+// 40.4.
 float tiled_us(int64_t M, int64_t N, int64_t K, int bm, int bn, float c, int splits) {
   const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn), nk = K / KB;
   const int64_t rounds = (tiles * splits + 255) / 256;
