@@ -970,7 +970,7 @@ typedef ring::G<2, 4, 1, 1, 6, 3, 1> R64x128nt;
 typedef ring::G<2, 4, 2, 1, 4, 4> R128x128;
 typedef ring::G<2, 4, 2, 2, 3, 3> R128x256;
 
-enum Kind { kFew, k64x128, k128x128, k128x256, k256x256 };
+enum Kind { kFew, kFew2, k64x128, k128x128, k128x256, k256x256 };
 
 struct Plan {
   Kind kind;
@@ -981,31 +981,29 @@ struct Plan {
 constexpr int64_t kPastCache = int64_t(1) << 27;
 
 // The kernel and split with the least expected time, in us, by a model whose
-// constants were fitted to the times of all of them at 189 sizes (1 to 4096
-// tokens, weights of 128 x 384 to 28672 x 4096): its choice is within 0.8% of
-// the fastest on average, 26% at worst (1440 x 3551 x 384, where C's bytes rule). Few tokens: a start, and for each
-// round of 256 work-groups and 1024 k a time that grows with M. Tiles: a start,
-// and for each round of 256 tiles c a k-tile and an epilogue by the tile's
-// area, but no faster than B from memory, the operands of all tiles through
-// the caches, or the arithmetic; a split of k adds a launch and its partial
-// sums. Measured, for example, at 1024 x 4096 (N x K) and 64 tokens: few 11.0,
-// 64 x 128 tiles 8.8, split in eight 8.1; at 6144 x 4096 and 512 tokens 22.8 /
-// 16.3 / 22.8 / 39.9 for the four tiles, and at 1024 tokens 39.0 / 32.7 / 27.2 /
-// 40.4.
+// constants were fitted to the times of all of them at 279 sizes (1 to 4096
+// tokens, weights of 128 x 256 to 28672 x 4096): its choice is within 0.7% of
+// the fastest on average, 26% at worst (1983 x 3220 x 256, where C's bytes
+// rule). Few tokens: a start, and for each round of 256 work-groups and 1024 k
+// a time that grows with M; two groups of 16 rows of B to each load of A where
+// that still gives most CUs a work-group (us, one group / two: 6144 x 4096, M = 4
+// 7.5 / 7.0, M = 16 9.4 / 8.1, M = 64 20.3 / 14.3; 1024 x 4096, M = 16 5.4 /
+// 7.4). Tiles: a start, and for each round of 256 tiles c a k-tile and an
+// epilogue by the tile's area, but no faster than B from memory, the operands
+// of all tiles through the caches, or the arithmetic; a split of k adds a launch
+// and its partial sums. Measured, for example, at 1024 x 4096 (N x K) and 64
+// tokens: few 11.0, 64 x 128 tiles 8.8, split in eight 8.1; at 6144 x 4096 and
+// 512 tokens 22.8 / 16.3 / 22.8 / 39.9 for the four tiles, and at 1024 tokens
+// 39.0 / 32.7 / 27.2 / 40.4.
 float tiled_us(int64_t M, int64_t N, int64_t K, int bm, int bn, float c, int splits) {
   const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn), nk = K / KB;
   const int64_t rounds = (tiles * splits + 255) / 256;
-  float t = (float)rounds * ((float)((nk + splits - 1) / splits) * c + 4.35f * (float)(bm * bn) / 65536.f);
-  t = fmaxf(t, (float)N * K / (N * K >= kPastCache ? 6.31e6f : 8e6f));
-  t = fmaxf(t, (float)(tiles * nk) * ((bm + bn) * KB) / 13.1e6f);
-  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 2.33e9f);
-  return 2.17f + t + (splits > 1 ? 3.58f + (float)splits * M * N * 8.f / 3.19e6f : 0.f);
+  float t = (float)rounds * ((float)((nk + splits - 1) / splits) * c + 5.96f * (float)(bm * bn) / 65536.f);
+  t = fmaxf(t, (float)N * K / (N * K >= kPastCache ? 8.32e6f : 9.38e6f));
+  t = fmaxf(t, (float)(tiles * nk) * ((bm + bn) * KB) / 14.5e6f);
+  t = fmaxf(t, (float)tiles * bm * bn * 2.f * K / 2.99e9f);
+  return 2.17f + t + (splits > 1 ? 4.08f + (float)splits * M * N * 8.f / 2.38e6f : 0.f);
 }
-
-// Two groups of 16 rows of B to each load of A where that still gives most CUs
-// a work-group (us, one group / two: 6144 x 4096, M = 4 7.5 / 7.0, M = 16 9.4 /
-// 8.1, M = 64 20.3 / 14.3; 1024 x 4096, M = 16 5.4 / 7.4).
-bool two_groups(int64_t N) { return N > 4608; }
 
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   Plan best{k64x128, 1};
@@ -1018,21 +1016,22 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   };
   if (M > 64) {  // (larger tiles would be rows past the end)
     offer(k128x128, 1, tiled_us(M, N, K, 128, 128, 0.462f, 1));
-    offer(k128x256, 1, tiled_us(M, N, K, 128, 256, 0.732f, 1));
+    offer(k128x256, 1, tiled_us(M, N, K, 128, 256, 0.823f, 1));
     offer(k256x256, 1, tiled_us(M, N, K, 256, 256, 1.01f, 1));
   }
   for (int s : {2, 3, 4, 6, 8}) {  // splits of at least 4 k-tiles
     if (s * 4 > K / KB || M > 4096) break;  // (rows are a grid dimension of the sums)
     offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.347f, s));
     if (M > 64 && s <= 4) offer(k128x128, s, tiled_us(M, N, K, 128, 128, 0.462f, s));
-    if (M > 64 && s <= 2) offer(k128x256, s, tiled_us(M, N, K, 128, 256, 0.732f, s));
+    if (M > 64 && s <= 2) offer(k128x256, s, tiled_us(M, N, K, 128, 256, 0.823f, s));
   }
-  if (M <= 64) {
-    const int64_t rows = two_groups(N) ? 8192 : 4096;  // 256 work-groups' rows of B
-    const float per = (0.426f + 0.0291f * M) * (!two_groups(N) ? 1.f : M <= 16 && K <= 1024 ? 1.72f : 1.39f);
-    const float mem = (float)N * K / (N * K >= kPastCache ? 4.45e6f : 6.15e6f);
-    offer(kFew, 1, 2.58f + fmaxf((float)((N + rows - 1) / rows) * K / 1024.f * per, mem));
-  }
+  if (M <= 64)
+    for (int g : {1, 2}) {
+      const float rounds = (float)((N + 4096 * g - 1) / (4096 * g));
+      const float per = g == 1 ? 0.449f + 0.0432f * M : 0.713f + 0.0552f * M;
+      const float mem = (float)N * K / (N * K >= kPastCache ? 6.64e6f : 8.81e6f);
+      offer(g == 1 ? kFew : kFew2, 1, 2.35f + fmaxf(rounds * K / 1024.f * per, mem));
+    }
   return best;
 }
 
@@ -1042,13 +1041,15 @@ hipError_t launch_out(const Args& P, void* ws, hipStream_t st) {
   const Plan plan = plan_of(P.M, P.N, P.K);
   switch (plan.kind) {
     case kFew:
-      // few chunks of k leave 8 waves half idle (22741 x 512, M = 1: 4.4 against 5.2)
-      if (P.M <= 16 && two_groups(P.N) && P.K <= 1024) return few::launch<4, 4, 1, 2, OUT>(P, st);
-      if (P.M <= 16)
-        return two_groups(P.N) ? few::launch<8, 4, 1, 2, OUT>(P, st) : few::launch<8, 4, 1, 1, OUT>(P, st);
-      if (P.M <= 32)
-        return two_groups(P.N) ? few::launch<4, 4, 2, 2, OUT>(P, st) : few::launch<8, 4, 2, 1, OUT>(P, st);
-      return two_groups(P.N) ? few::launch<4, 4, 4, 2, OUT>(P, st) : few::launch<8, 2, 4, 1, OUT>(P, st);
+      if (P.M <= 16) return few::launch<8, 4, 1, 1, OUT>(P, st);
+      if (P.M <= 32) return few::launch<8, 4, 2, 1, OUT>(P, st);
+      return few::launch<8, 2, 4, 1, OUT>(P, st);
+    case kFew2:
+      // few chunks of k leave 8 waves half idle (22741 x 512, M = 1: 4.4 against 5.3)
+      if (P.M <= 16 && P.K <= 1024) return few::launch<4, 4, 1, 2, OUT>(P, st);
+      if (P.M <= 16) return few::launch<8, 4, 1, 2, OUT>(P, st);
+      if (P.M <= 32) return few::launch<4, 4, 2, 2, OUT>(P, st);
+      return few::launch<4, 4, 4, 2, OUT>(P, st);
     case k64x128:
       // One tile-row reads B once. A large weight comes from HBM each time, and
       // past the caches is faster (28672 x 4096, M = 64: 23.8 against 28.3 us);
