@@ -370,10 +370,10 @@ __device__ __forceinline__ void fetch_factors(uint8_t* lds, const Args& P, int64
 
 // ------------------------------------------------------- few tokens (M <= 16 MG)
 // The weight's bytes are the work. A work-group owns 16 rows of B and its W
-// waves split k: chunk c of 64 bytes of the 16 rows belongs to wave c % W,
-// loaded straight into registers in the MFMA's layout (lane l: row l % 16, 16
-// bytes at 16 (l / 16)), so W waves read 64 W consecutive bytes of each row.
-// A wave keeps U chunks in flight: a chunk's registers are loaded again right
+// waves split k: of the chunks of 64 bytes of the 16 rows, 2 c and 2 c + 1 belong
+// to wave c % W, loaded straight into registers in the MFMA's layout (lane l:
+// row l % 16, 16 bytes at 16 (l / 16)), so W waves read 128 W consecutive bytes
+// of each row. A wave keeps U chunks in flight: a chunk's registers are loaded again right
 // after its MFMA. Chunks past the end are loads out of the buffer's range
 // (zero, no traffic), so that a round of U has no branches. The tokens (A) come
 // from the caches. Partial sums meet in LDS. Measured: 4096 x 14336, one token
@@ -630,9 +630,7 @@ __global__ __launch_bounds__(T::NT) void gemm_kernel(Args P, int splits, int* pa
   // (each wave's own DMAs of it have landed, the later ones stay in flight)
   // and retires slot S (each wave's reads of it are done), which takes k-tile
   // k + NS: the first of its SP parts here, the others with the first k-steps
-  // of k-tile k + 1. (Fragments read two k-steps ahead, with the barrier in
-  // the middle, ran the 64 x 128 tile 4% faster and the larger ones 5-12%
-  // slower.)
+  // of k-tile k + 1.
   auto part_of = [&](auto S, auto Q, int k) {  // part Q of k-tile k into slot S
     constexpr int u0 = NB * Q.value / T::SP, u1 = NB * (Q.value + 1) / T::SP;
     if constexpr (Q.value < T::SP)
@@ -1023,7 +1021,6 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
     if (s * 4 > K / KB || M > 4096) break;  // (rows are a grid dimension of the sums)
     offer(k64x128, s, tiled_us(M, N, K, 64, 128, 0.347f, s));
     if (M > 64 && s <= 4) offer(k128x128, s, tiled_us(M, N, K, 128, 128, 0.462f, s));
-    if (M > 64 && s <= 2) offer(k128x256, s, tiled_us(M, N, K, 128, 256, 0.823f, s));
   }
   if (M <= 64)
     for (int g : {1, 2}) {
