@@ -36,7 +36,8 @@ void check(int status, const char* where) {
   throw py::error_already_set();
 }
 
-// The codes have no gradient: a call that autograd would have to record is refused.
+// Codes and their products have no gradient, in their scales and bias neither:
+// a call that autograd would have to record is refused.
 void no_gradient(const char* where, std::initializer_list<const Tensor*> inputs) {
   if (!at::GradMode::is_enabled()) return;
   for (const Tensor* t : inputs)
@@ -272,6 +273,7 @@ const void* codes_of(const Tensor& t, int64_t K, const char* name, const Tensor*
 
 Tensor gemm(const Tensor& a, const Tensor& sa, const Tensor& b, const Tensor& sb, const Maybe& bias, int64_t K,
             at::ScalarType out) {
+  no_gradient("int8_gemm", {&sa, &sb, ptr(bias)});
   int64_t lda, ldb;
   const void* pa = codes_of(a, K, "a", nullptr, &lda);
   const void* pb = codes_of(b, K, "b", &a, &ldb);
@@ -319,6 +321,7 @@ Tensor int8_linear(const Tensor& x, const Tensor& w, const Tensor& sw, const May
                    std::optional<at::ScalarType> out) {
   TORCH_CHECK_VALUE(x.dim() >= 1, "x must have a dimension");
   check_weight(w, x.size(-1), "weight codes");
+  no_gradient("int8_linear", {&x, &sw, ptr(bias)});
   const Operand q = quantize(x, {});
   return as(product(q, w, sw, bias, out.value_or(x.scalar_type())), x);
 }
@@ -330,6 +333,7 @@ py::tuple int8_mlp(const Tensor& x, const Maybe& weight, double eps, const Tenso
   TORCH_CHECK_VALUE(gu.size(0) % 2 == 0, "gate_up must have an even number of rows, got ", gu.size(0));
   const int64_t F = gu.size(0) / 2;
   check_weight(down, F, "down codes");
+  no_gradient("int8_mlp", {&x, ptr(weight), ptr(residual), &gus, &downs});
   Tensor h;
   const Operand q = norm_int8(x, weight, eps, residual, &h);
   const Tensor mid = product(q, gu, gus, {}, x.scalar_type());

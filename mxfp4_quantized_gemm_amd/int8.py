@@ -8,7 +8,8 @@ serve (any number of rows from one, any width).
 
 An operand is int8 [rows][pitch]: the pitch is the width rounded up to a
 multiple of 128, with zero codes past the width, which a product runs over.
-Inference only (the codes have no gradient). Marshalling only: every step
+Inference only: a call in which an input, a scale or the bias requires a gradient
+is refused (torch.no_grad() or detached tensors). Marshalling only: every step
 runs in the library's kernels.
 """
 from __future__ import annotations

@@ -1,0 +1,40 @@
+"""Calls whose derivative the library does not have refuse the inputs that
+would need it (no GPU: the refusals come before any other check)."""
+import pytest
+import torch
+
+from mxfp4_quantized_gemm_amd import int8, norm
+
+
+def operands():
+    """x [4][64], codes and scales of 8 rows, a bias, all in host memory."""
+    return (torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(8, 128, dtype=torch.int8), torch.ones(8),
+            torch.zeros(8))
+
+
+def leaf(t):
+    return t.clone().requires_grad_(True)
+
+
+def products(mark):
+    """Every call with a product, with one of its scales or its bias marked by ``mark``."""
+    x, q, s, b = operands()
+    down, ds = torch.zeros(64, 128, dtype=torch.int8), torch.ones(64)
+    w = torch.ones(64, dtype=torch.bfloat16)
+    return {
+        "gemm a_scales": lambda: int8.int8_gemm(q, mark(s), q, s),
+        "gemm b_scales": lambda: int8.int8_gemm(q, s, q, mark(s)),
+        "gemm bias": lambda: int8.int8_gemm(q, s, q, s, bias=mark(b)),
+        "linear w_scales": lambda: int8.int8_linear(x, q, mark(s)),
+        "linear bias": lambda: int8.int8_linear(x, q, s, bias=mark(b)),
+        "mlp gate_up_scales": lambda: int8.int8_mlp(x, w, 1e-5, q, mark(s), down, ds),
+        "mlp down_scales": lambda: int8.int8_mlp(x, w, 1e-5, q, s, down, mark(ds)),
+    }
+
+
+@pytest.mark.parametrize("call", list(products(leaf)))
+def test_products_refuse_to_be_recorded(call):
+    with pytest.raises(RuntimeError, match="no gradient"):
+        products(leaf)[call]()
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU memory"):
+        products(leaf)[call]()
