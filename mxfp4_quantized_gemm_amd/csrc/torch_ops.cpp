@@ -36,9 +36,18 @@ void check(int status, const char* where) {
   throw py::error_already_set();
 }
 
+// A forward-mode tangent of an input would be dropped, which is a derivative of
+// zero. (no_grad() does not switch forward mode off.)
+void no_tangent(const char* where, std::initializer_list<const Tensor*> inputs) {
+  for (const Tensor* t : inputs)
+    TORCH_CHECK(t == nullptr || !t->defined() || !t->_fw_grad(0).defined(), where,
+                " has no forward-mode derivative");
+}
+
 // Codes and their products have no gradient, in their scales and bias neither:
 // a call that autograd would have to record is refused.
 void no_gradient(const char* where, std::initializer_list<const Tensor*> inputs) {
+  no_tangent(where, inputs);
   if (!at::GradMode::is_enabled()) return;
   for (const Tensor* t : inputs)
     TORCH_CHECK(t == nullptr || !t->requires_grad(), where,
@@ -169,6 +178,7 @@ struct RMSNormFunction : torch::autograd::Function<RMSNormFunction> {
       dx = dh;
       if (want_w) dw = at::zeros_like(weight);
     } else {
+      no_tangent("the gradient of rms_norm", {&dy, &dh});
       const c10::DeviceGuard guard(h.device());
       const Rows rh = rows_of(h, "h"), ry = rows_of(dy, "dy");
       const bool more = dh.defined();
@@ -193,6 +203,7 @@ struct RMSNormFunction : torch::autograd::Function<RMSNormFunction> {
 };
 
 py::object rms_norm(const Tensor& x, const Maybe& weight, double eps, const Maybe& residual) {
+  no_tangent("rms_norm", {&x, ptr(weight), ptr(residual)});
   const bool grad = at::GradMode::is_enabled() &&
                     (x.requires_grad() || (has(residual) && residual->requires_grad()) ||
                      (has(weight) && weight->requires_grad()));

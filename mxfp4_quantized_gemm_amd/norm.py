@@ -17,7 +17,8 @@ from ._load import ops
 
 
 def rms_norm(x, weight=None, eps=1e-5, residual=None):
-    """y, or (y, h) with a residual; differentiable once in x, residual and weight."""
+    """y, or (y, h) with a residual; differentiable once in x, residual and weight,
+    in reverse mode (forward-mode tangents are refused)."""
     return ops.rms_norm(x, weight, eps, residual)
 
 

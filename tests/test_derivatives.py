@@ -38,3 +38,35 @@ def test_products_refuse_to_be_recorded(call):
         products(leaf)[call]()
     with torch.no_grad(), pytest.raises(ValueError, match="GPU memory"):
         products(leaf)[call]()
+
+
+# ------------------------------------------------------------ forward mode
+def dual(t):
+    import torch.autograd.forward_ad as fwd
+    return fwd.make_dual(t.clone(), torch.ones_like(t))
+
+
+def rows(mark):
+    """The norm and the quantizers, with one of their inputs marked by ``mark``."""
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    return {
+        "norm x": lambda: norm.rms_norm(mark(x), w),
+        "norm weight": lambda: norm.rms_norm(x, mark(w)),
+        "norm residual": lambda: norm.rms_norm(x, w, residual=mark(x)),
+        "norm x, recorded too": lambda: norm.rms_norm(mark(x), w.clone().requires_grad_(True)),
+        "norm codes x": lambda: norm.rms_norm_int8(mark(x), w),
+        "norm codes weight": lambda: norm.rms_norm_int8(x, mark(w)),
+        "norm codes residual": lambda: norm.rms_norm_int8(x, w, residual=mark(x)),
+        "codes x": lambda: int8.int8_quantize(mark(x)),
+        "codes gate": lambda: int8.int8_quantize(x, gate=mark(x)),
+    }
+
+
+@pytest.mark.parametrize("call", [*rows(leaf), *products(leaf)])
+def test_tangents_are_refused(call):
+    """A forward-mode tangent would be dropped: a derivative of zero."""
+    import torch.autograd.forward_ad as fwd
+    with fwd.dual_level():
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad), pytest.raises(RuntimeError, match="forward-mode"):
+                {**rows(dual), **products(dual)}[call]()
