@@ -6,6 +6,7 @@
 // in Python (ctypes) cost 8 us a call and the norm's gradient 135 us.
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 #include <torch/extension.h>
 
 #include <optional>
@@ -36,6 +37,12 @@ void check(int status, const char* where) {
   throw py::error_already_set();
 }
 
+// torch.jit.trace would record the outputs' allocation alone: replays of it would
+// return memory that nothing wrote.
+void no_trace(const char* where) {
+  TORCH_CHECK(!torch::jit::tracer::isTracing(), where, " cannot be recorded by torch.jit.trace");
+}
+
 // A forward-mode tangent of an input would be dropped, which is a derivative of
 // zero. (no_grad() does not switch forward mode off.)
 void no_tangent(const char* where, std::initializer_list<const Tensor*> inputs) {
@@ -47,6 +54,7 @@ void no_tangent(const char* where, std::initializer_list<const Tensor*> inputs) 
 // Codes and their products have no gradient, in their scales and bias neither:
 // a call that autograd would have to record is refused.
 void no_gradient(const char* where, std::initializer_list<const Tensor*> inputs) {
+  no_trace(where);
   no_tangent(where, inputs);
   if (!at::GradMode::is_enabled()) return;
   for (const Tensor* t : inputs)
@@ -203,6 +211,7 @@ struct RMSNormFunction : torch::autograd::Function<RMSNormFunction> {
 };
 
 py::object rms_norm(const Tensor& x, const Maybe& weight, double eps, const Maybe& residual) {
+  no_trace("rms_norm");
   no_tangent("rms_norm", {&x, ptr(weight), ptr(residual)});
   const bool grad = at::GradMode::is_enabled() &&
                     (x.requires_grad() || (has(residual) && residual->requires_grad()) ||

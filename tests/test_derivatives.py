@@ -70,3 +70,16 @@ def test_tangents_are_refused(call):
         for grad in (True, False):
             with torch.set_grad_enabled(grad), pytest.raises(RuntimeError, match="forward-mode"):
                 {**rows(dual), **products(dual)}[call]()
+
+
+# ------------------------------------------------------------ tracing
+@pytest.mark.filterwarnings("ignore::DeprecationWarning")
+@pytest.mark.parametrize("call", [*rows(leaf), *products(leaf)])
+def test_tracing_is_refused(call):
+    """A trace would hold the outputs' allocation alone, and its replays return
+    memory that nothing wrote."""
+    def traced(t):
+        with torch.no_grad():
+            return {**rows(lambda a: a), **products(lambda a: a)}[call]()
+    with pytest.raises(RuntimeError, match="trace"):
+        torch.jit.trace(traced, (torch.zeros(1),), check_trace=False)
