@@ -48,7 +48,8 @@ def int8_mlp(x, norm_weight, eps, gate_up, gate_up_scales, down, down_scales, re
 class Int8Linear(torch.nn.Module):
     """Linear layer with int8 weight codes [out][in rounded up to 128], a
     scale for each output channel and an optional fp32 bias (buffers: this
-    layer is not trained)."""
+    layer is not trained). Casts of a model (bfloat16(), to(dtype), ...) leave
+    their types and values as they are."""
 
     def __init__(self, in_features, out_features, bias=False, device=None):
         super().__init__()
@@ -68,6 +69,15 @@ class Int8Linear(torch.nn.Module):
         if bias is not None:
             layer.bias = bias.detach().float()
         return layer
+
+    def _apply(self, fn, recurse=True):
+        # Module's casts and moves come through here: take the moves only
+        kept = dict(self._buffers)
+        super()._apply(fn, recurse)
+        for name, b in kept.items():
+            if b is not None and self._buffers[name].dtype != b.dtype:
+                self._buffers[name] = b.to(self._buffers[name].device)
+        return self
 
     def forward(self, x):
         if x.shape[-1] != self.in_features:
