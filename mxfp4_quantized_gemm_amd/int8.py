@@ -63,11 +63,14 @@ class Int8Linear(torch.nn.Module):
     @classmethod
     @torch.no_grad()
     def from_weight(cls, weight, bias=None):
-        """From a weight [out][in] in GPU memory (a Linear's or MXFP4Linear's)."""
+        """From a weight [out][in] in GPU memory (a Linear's or MXFP4Linear's) and
+        its bias; both are copied."""
+        if bias is not None and bias.shape != weight.shape[:1]:
+            raise ValueError(f"bias must be [{weight.size(0)}], got {list(bias.shape)}")
         layer = cls(weight.size(1), weight.size(0), bias is not None, weight.device)
         layer.weight, layer.scales = int8_quantize(weight.detach())
         if bias is not None:
-            layer.bias = bias.detach().float()
+            layer.bias.copy_(bias)
         return layer
 
     def _apply(self, fn, recurse=True):

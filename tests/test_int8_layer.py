@@ -38,3 +38,21 @@ def test_moves_of_a_model_move_the_layer():
     assert all(b.device.type == "meta" for b in m.buffers())
     assert [b.dtype for b in m.buffers()] == [torch.int8, torch.float32, torch.float32]
     assert int8.Int8Linear(200, 6).half().bias is None
+
+
+def test_from_weight_copies_the_bias(monkeypatch):
+    """Steps of an optimizer on the source's bias must not reach the layer, whose codes they do not reach."""
+    monkeypatch.setattr(int8, "int8_quantize", lambda w: (torch.zeros(len(w), 256, dtype=torch.int8), torch.ones(len(w))))
+    source = torch.nn.Linear(200, 6)
+    want = source.bias.detach().clone()
+    for bias in (source.bias, source.bias.to(torch.bfloat16), torch.stack((want, want), 1)[:, 0]):
+        m = int8.Int8Linear.from_weight(source.weight, bias)
+        with torch.no_grad():
+            held = bias.detach().float().clone()
+            bias += 1
+        assert m.bias.dtype == torch.float32 and m.bias.is_contiguous() and not m.bias.requires_grad
+        assert torch.equal(m.bias, held)
+        with torch.no_grad():
+            bias -= 1
+    with pytest.raises(ValueError, match="bias"):
+        int8.Int8Linear.from_weight(source.weight, torch.zeros(1))
