@@ -408,7 +408,9 @@ size_t mxfp4_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
  * mxfp4_int8_quantize -- codes and scales of the rows of x, as
  * mxfp4_rmsnorm_int8 makes them of y. With `gate` (same shape and type, NULL:
  * none) of silu(gate) x instead, the gated activation of a feed-forward
- * block, in fp32 (relative error of silu below 2^-19 + |gate| 2^-23).
+ * block, in fp32 (relative error below 2^-19 + |gate| 2^-23 for any gate,
+ * where silu(gate) x is a normal fp32 number, and a step of the smallest
+ * subnormal below; a gate of -infinity counts as an infinity).
  */
 int mxfp4_int8_quantize(const void* x, int64_t x_ld, const void* gate, int64_t gate_ld,
                         int64_t rows, int64_t cols, int dtype, void* codes, int64_t codes_ld,

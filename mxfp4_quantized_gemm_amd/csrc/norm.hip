@@ -355,9 +355,19 @@ __device__ __forceinline__ void write_codes(const float (&v)[R][V], uint32_t* re
 // silu(g) u = g u / (1 + exp(-g)), by the hardware's base-2 exponential and
 // reciprocal (each within about one ulp; the rounded argument g log2(e) adds
 // at most |g| 2^-24 to the relative error): far below half a step of a code.
+// Past t = -g log2(e) = kFar the exponential and the reciprocal leave fp32's
+// range, though g u 2^-t need not (any u): there 1 / (1 + 2^t) is 2^-kFar h h
+// with h = 2^((kFar - t) / 2), and the factors are taken in an order in which
+// none leaves the range before the result does (kFar - t is exact). 512 x 14336
+// bf16: 7.4 us with this branch and 7.6 without; 9.6 where all waves take it.
+constexpr float kFar = 120.f;
+__device__ __forceinline__ float exponent(float g) { return g * -1.44269504f; }
 __device__ __forceinline__ float swiglu(float g, float u) {
-  const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);
-  return g * __builtin_amdgcn_rcpf(1.f + e) * u;
+  return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(exponent(g))) * u;
+}
+__device__ __forceinline__ float swiglu_far(float g, float u) {
+  const float h = __builtin_amdgcn_exp2f(0.5f * (kFar - exponent(g)));
+  return g * 0x1p-120f * (h * u) * h;
 }
 
 constexpr int kNorm = 0, kNormInt8 = 1, kQuant = 2, kSwiglu = 3;
@@ -391,9 +401,19 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void row_kernel(RowArgs A) {
     float g[R][V];
     X::load(A.res, row * A.res_ld, A.cols, t, g);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
+      float far = 0.f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[i][k] = swiglu(g[i][k], v[i][k]);
+      for (int k = 0; k < V; ++k) far = fmaxf(far, exponent(g[i][k]));
+      if (far <= kFar) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][k] = swiglu(g[i][k], v[i][k]);
+      } else {  // a gate below -83: hardly ever
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          v[i][k] = exponent(g[i][k]) > kFar ? swiglu_far(g[i][k], v[i][k]) : swiglu(g[i][k], v[i][k]);
+      }
+    }
   }
   if constexpr (OP == kNorm || OP == kNormInt8) {
     if (A.res != nullptr) {
