@@ -61,12 +61,26 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n" + r.stderr)
 
 
+def _no_ops() -> str | None:
+    """What the torch binding needs and this machine lacks, if anything."""
+    if shutil.which("g++") is None:
+        return "g++ is missing"
+    try:
+        import torch  # noqa: F401
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        return f"torch does not import ({e})"
+    if not any(os.path.exists(os.path.join(d, "torch", "extension.h")) for d in cpp_extension.include_paths()):
+        return "torch's headers are missing"
+    return None
+
+
 def _compile_ops() -> str:
     """torch_ops.cpp -> object: host code against torch's and HIP's headers."""
     import torch
     from torch.utils import cpp_extension
     out = os.path.join(BUILD, "torch_ops.cpp.o")
-    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-c", "-D__HIP_PLATFORM_AMD__",
+    _run([shutil.which("g++"), "-O2", "-std=c++17", "-fPIC", "-c", "-D__HIP_PLATFORM_AMD__",
           "-DUSE_ROCM", "-DTORCH_EXTENSION_NAME=_ops", "-DTORCH_API_INCLUDE_EXTENSION_H",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *(f for d in [*cpp_extension.include_paths(), os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
@@ -78,26 +92,35 @@ def _compile_ops() -> str:
 def _link_ops(obj: str) -> None:
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    _run([shutil.which("g++") or "g++", "-shared", "-o", OPS + ".tmp", obj, "-L" + PKG, "-l:libmxfp4.so",
+    _run([shutil.which("g++"), "-shared", "-o", OPS + ".tmp", obj, "-L" + PKG, "-l:libmxfp4.so",
           "-L" + libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs], "linking _ops.so")
     os.replace(OPS + ".tmp", OPS)
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source and link both libraries; returns libmxfp4.so's path."""
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ops = ex.submit(_compile_ops)
-        objs = list(ex.map(_compile, SOURCES))
-        ops = ops.result()
+def _link(objs) -> None:
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stderr)
+    _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs], "linking libmxfp4.so")
     os.replace(tmp, LIB)
-    _link_ops(ops)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source and link both libraries; returns libmxfp4.so's path.
+
+    libmxfp4.so is linked first and needs nothing of the torch binding; on a
+    machine without g++ or torch's headers it is built alone (the norm and 8-bit
+    modules then raise when they are imported)."""
+    os.makedirs(BUILD, exist_ok=True)
+    lacking = _no_ops()
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ops = None if lacking else ex.submit(_compile_ops)
+        _link(list(ex.map(_compile, SOURCES)))
+        if ops:
+            _link_ops(ops.result())
+    if lacking:
+        sys.stderr.write(f"_ops.so (norm and 8-bit operators from Python) is not built: {lacking}\n")
+        if os.path.exists(OPS):  # it may not fit the new library
+            os.remove(OPS)
     if verbose:
         print(f"built {LIB}")
     return LIB
