@@ -491,10 +491,16 @@ def _dt(dtype):
         raise TypeError(f"type must be float32, bfloat16 or float16, got {dtype}") from None
 
 
-def _mat(t, rows, cols, dtype, name):
-    """Address and row pitch of a [rows][cols] matrix on the GPU."""
+def _on(t, device, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must live in GPU memory")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+
+
+def _mat(t, rows, cols, dtype, name, device):
+    """Address and row pitch of a [rows][cols] matrix on the GPU."""
+    _on(t, device, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
@@ -505,12 +511,11 @@ def _mat(t, rows, cols, dtype, name):
     return t.data_ptr(), max(s0, cols)
 
 
-def _vec(t, n, dtype, name):
+def _vec(t, n, dtype, name, device):
     """Address of a vector of at least n values (None: 0)."""
     if t is None:
         return 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live in GPU memory")
+    _on(t, device, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() < n or not t.is_contiguous():
@@ -535,17 +540,17 @@ def _run(fn, args, device, stream):
 
 
 def _norm_args(x, residual, weight, eps, h):
-    dtype = x.dtype
+    dtype, dev = x.dtype, x.device
     rows, cols = x.shape
-    xp, xl = _mat(x, rows, cols, dtype, "x")
-    rp, rl = (0, cols) if residual is None else _mat(residual, rows, cols, dtype, "residual")
-    hp, hl = (0, cols) if h is None else _mat(h, rows, cols, dtype, "h")
+    xp, xl = _mat(x, rows, cols, dtype, "x", dev)
+    rp, rl = (0, cols) if residual is None else _mat(residual, rows, cols, dtype, "residual", dev)
+    hp, hl = (0, cols) if h is None else _mat(h, rows, cols, dtype, "h", dev)
     wt, wp = dtype, 0
     if weight is not None:
         wt = weight.dtype
         if weight.numel() != cols:
             raise ValueError(f"weight must hold {cols} values, holds {weight.numel()}")
-        wp = _vec(weight, cols, wt, "weight")
+        wp = _vec(weight, cols, wt, "weight", dev)
     return (xp, xl, rp, rl, wp, _dt(wt), rows, cols, eps, _dt(dtype), hp, hl), rows, cols
 
 
@@ -554,7 +559,8 @@ def mxfp4_rmsnorm(x, residual, weight, eps, h, y, rstd, stream=None):
     args, rows, cols = _norm_args(x, residual, weight, eps, h)
     import torch
     _run(load_library().mxfp4_rmsnorm,
-         (*args, *_mat(y, rows, cols, x.dtype, "y"), _vec(rstd, rows, torch.float32, "rstd")),
+         (*args, *_mat(y, rows, cols, x.dtype, "y", x.device),
+          _vec(rstd, rows, torch.float32, "rstd", x.device)),
          x.device, stream)
 
 
@@ -563,30 +569,30 @@ def mxfp4_rmsnorm_int8(x, residual, weight, eps, h, codes, scales, stream=None):
     import torch
     args, rows, cols = _norm_args(x, residual, weight, eps, h)
     _run(load_library().mxfp4_rmsnorm_int8,
-         (*args, *_codes(codes, rows, cols), _vec(scales, rows, torch.float32, "scales")),
+         (*args, *_codes(codes, rows, cols, x.device), _vec(scales, rows, torch.float32, "scales", x.device)),
          x.device, stream)
 
 
-def _codes(t, rows, cols):
+def _codes(t, rows, cols, device):
     import torch
     if t.dim() != 2 or t.size(1) < cols:
         raise ValueError(f"codes must be [{rows}][{cols} or more], got {list(t.shape)}")
-    return _mat(t, rows, t.size(1), torch.int8, "codes")
+    return _mat(t, rows, t.size(1), torch.int8, "codes", device)
 
 
 def mxfp4_rmsnorm_bwd(dy, dh, h, weight, rstd, dx, dweight, ws, stream=None):
     """Gradients of mxfp4_rmsnorm (dh, weight, dweight and ws may be None)."""
     import torch
     rows, cols = h.shape
-    dtype = h.dtype
+    dtype, dev = h.dtype, h.device
     wt = dtype if weight is None and dweight is None else (dweight if weight is None else weight).dtype
-    args = (*_mat(dy, rows, cols, dtype, "dy"),
-            *((0, cols) if dh is None else _mat(dh, rows, cols, dtype, "dh")),
-            *_mat(h, rows, cols, dtype, "h"), _vec(weight, cols, wt, "weight"), _dt(wt),
-            _vec(rstd, rows, torch.float32, "rstd"), rows, cols, _dt(dtype),
-            *_mat(dx, rows, cols, dtype, "dx"), _vec(dweight, cols, wt, "dweight"),
-            _vec(ws, 0, torch.uint8, "ws"), 0 if ws is None else ws.numel())
-    _run(load_library().mxfp4_rmsnorm_bwd, args, h.device, stream)
+    args = (*_mat(dy, rows, cols, dtype, "dy", dev),
+            *((0, cols) if dh is None else _mat(dh, rows, cols, dtype, "dh", dev)),
+            *_mat(h, rows, cols, dtype, "h", dev), _vec(weight, cols, wt, "weight", dev), _dt(wt),
+            _vec(rstd, rows, torch.float32, "rstd", dev), rows, cols, _dt(dtype),
+            *_mat(dx, rows, cols, dtype, "dx", dev), _vec(dweight, cols, wt, "dweight", dev),
+            _vec(ws, 0, torch.uint8, "ws", dev), 0 if ws is None else ws.numel())
+    _run(load_library().mxfp4_rmsnorm_bwd, args, dev, stream)
 
 
 def mxfp4_rmsnorm_bwd_workspace_bytes(rows, cols):
@@ -597,10 +603,11 @@ def mxfp4_int8_quantize(x, gate, codes, scales, stream=None):
     """Int8 codes [rows][>= cols] and scales [rows] of ``x``, or of ``silu(gate) * x``."""
     import torch
     rows, cols = x.shape
-    args = (*_mat(x, rows, cols, x.dtype, "x"),
-            *((0, cols) if gate is None else _mat(gate, rows, cols, x.dtype, "gate")),
-            rows, cols, _dt(x.dtype), *_codes(codes, rows, cols),
-            _vec(scales, rows, torch.float32, "scales"))
+    dev = x.device
+    args = (*_mat(x, rows, cols, x.dtype, "x", dev),
+            *((0, cols) if gate is None else _mat(gate, rows, cols, x.dtype, "gate", dev)),
+            rows, cols, _dt(x.dtype), *_codes(codes, rows, cols, x.device),
+            _vec(scales, rows, torch.float32, "scales", x.device))
     _run(load_library().mxfp4_int8_quantize, args, x.device, stream)
 
 
@@ -609,12 +616,12 @@ def mxfp4_int8_gemm(A, a_scales, B, b_scales, bias, C, ws, stream=None):
     import torch
     M, K = A.shape
     N = B.size(0)
-    f32 = torch.float32
-    args = (*_mat(A, M, K, torch.int8, "A"), _vec(a_scales, M, f32, "a_scales"),
-            *_mat(B, N, K, torch.int8, "B"), _vec(b_scales, N, f32, "b_scales"),
-            _vec(bias, N, f32, "bias"), M, N, K, *_mat(C, M, N, C.dtype, "C"), _dt(C.dtype),
-            0 if ws is None else _vec(ws, 0, torch.uint8, "ws"), 0 if ws is None else ws.numel())
-    _run(load_library().mxfp4_int8_gemm, args, A.device, stream)
+    f32, dev = torch.float32, A.device
+    args = (*_mat(A, M, K, torch.int8, "A", dev), _vec(a_scales, M, f32, "a_scales", dev),
+            *_mat(B, N, K, torch.int8, "B", dev), _vec(b_scales, N, f32, "b_scales", dev),
+            _vec(bias, N, f32, "bias", dev), M, N, K, *_mat(C, M, N, C.dtype, "C", dev), _dt(C.dtype),
+            0 if ws is None else _vec(ws, 0, torch.uint8, "ws", dev), 0 if ws is None else ws.numel())
+    _run(load_library().mxfp4_int8_gemm, args, dev, stream)
 
 
 def mxfp4_int8_gemm_workspace_bytes(M, N, K):
