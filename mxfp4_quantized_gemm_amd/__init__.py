@@ -574,10 +574,18 @@ def mxfp4_rmsnorm_int8(x, residual, weight, eps, h, codes, scales, stream=None):
 
 
 def _codes(t, rows, cols, device):
+    """Address and pitch of codes [rows][cols or more]; the kernels write zero codes
+    from cols up to a multiple of 128, or up to the pitch."""
     import torch
     if t.dim() != 2 or t.size(1) < cols:
         raise ValueError(f"codes must be [{rows}][{cols} or more], got {list(t.shape)}")
-    return _mat(t, rows, t.size(1), torch.int8, "codes", device)
+    p, ld = _mat(t, rows, t.size(1), torch.int8, "codes", device)
+    if rows <= 1:  # one row has no pitch
+        ld = t.size(1)
+    if t.size(1) < min((cols + 127) // 128 * 128, ld):
+        raise ValueError(f"codes of a wider matrix must have the columns of their zero codes, "
+                         f"[{rows}][{(cols + 127) // 128 * 128}], got {list(t.shape)}")
+    return p, ld
 
 
 def mxfp4_rmsnorm_bwd(dy, dh, h, weight, rstd, dx, dweight, ws, stream=None):
