@@ -367,7 +367,8 @@ size_t mxfp4_workspace_bytes(int op, int64_t T, int64_t N, int64_t K);
  * y = (h r) weight in fp32, rounded to `dtype` once. weight [cols] is of
  * `dtype` or fp32 (weight_dtype), NULL for 1. h (the new residual stream) and
  * rstd ([rows], the r of every row, which mxfp4_rmsnorm_bwd reads) may be
- * NULL. 1 <= cols <= 32768. eps >= 0; an all-zero row with eps = 0 gives NaN.
+ * NULL. 1 <= cols <= 32768. eps >= 0; with eps = 0 an all-zero row gives NaN, and
+ * one with a root mean square below 2^-128, whose r leaves fp32's range, infinities.
  */
 int mxfp4_rmsnorm(const void* x, int64_t x_ld, const void* residual, int64_t residual_ld,
                   const void* weight, int weight_dtype, int64_t rows, int64_t cols, float eps,

@@ -57,10 +57,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // ------------------------------------------------------ general kernel
-// Any sizes, pitches and alignments: 64 x 64 tiles of C, 4 waves of one 32 x
+// Any sizes, pitches and alignments (within the entry point's limits): 64 x 64 tiles of C, 4 waves of one 32 x
 // 32 MFMA tile each, k in steps of 64 staged through LDS. 16 bytes of a row
 // are loaded at once where its address allows it, byte by byte where not and
-// at the row's end; rows and bytes past the operands are zero.
+// at the row's end; rows and bytes past the operands are zero. It is far from the
+// DMA kernels: 2048 x 6144 x 4112 in 157 us (their 2048 x 6144 x 4096: 58), and by
+// bytes, where rows are not 16-byte aligned, x 4100 in 2.3 ms.
 namespace gen {
 
 constexpr int BM = 64, BN = 64, KB = 64;
@@ -377,7 +379,7 @@ __device__ __forceinline__ void fetch_factors(uint8_t* lds, const Args& P, int64
 // after its MFMA. Chunks past the end are loads out of the buffer's range
 // (zero, no traffic), so that a round of U has no branches. The tokens (A) come
 // from the caches. Partial sums meet in LDS. Measured: 4096 x 14336, one token
-// in 10.5 us, 5.6 TB/s. B is read through the caches: past them (it is used
+// in 11.0-11.6 us with B from memory, 5.1-5.3 TB/s. B is read through the caches: past them (it is used
 // once) was slower whether it lay in the last-level cache (10.2 against 14.3)
 // or not (12.1 against 13.0).
 namespace few {
@@ -469,10 +471,14 @@ hipError_t launch(const Args& P, hipStream_t st) {
 // are fewer output tiles than CUs the k range is split over blockIdx.y: the
 // int32 partial sums go to the workspace and a second kernel adds them (the
 // sums are exact, so the split does not show in the result).
-// What bounds it: the LDS, written by DMA at 64 bytes a clock and read at 256,
-// not both at once. A k-tile of 64 x 128 (8 waves of 32 x 32) is 384 + 256
-// clocks and takes 0.26 us whether a third of the CUs work or all, beside 256
-// clocks of MFMAs; 128 x 128 with 8 waves of 64 x 32 is 512 + 384 (16 waves of
+// What bounds it, while the operands lie in the caches and up to half of the CUs
+// work: the LDS, written by DMA at 64 bytes a clock and read at 256, not both at
+// once. A k-tile of 64 x 128 (8 waves of 32 x 32) is 384 + 256 clocks beside 256 of
+// MFMAs, and takes 0.25-0.28 us on 64 to 128 CUs. Past that it is the operands' way
+// to the CUs: with all CUs at work 0.32-0.36 us a k-tile from the caches (24 KB to
+// each of 256 CUs: 17-19 TB/s), and 0.44-0.50 us, on 128 CUs too, where the operands
+// come from memory (512 x 4096 x 14336, 112 k-tiles: 39 us the one way, 52 the
+// other). Tiles that need fewer operand bytes follow; 128 x 128 with 8 waves of 64 x 32 is 512 + 384 (16 waves of
 // 32 x 32: 512 + 512; 512 x 6144 x 4096 16.6 against 17.4 us), 128 x 256 with 8
 // waves of 64 x 64 is 768 + 512 (16 of 32 x 64: 768 + 768; 1024 x 6144 x 4096
 // 27.1 against 28.0). Fragments read a whole k-tile ahead, and rows touched in
@@ -979,9 +985,10 @@ struct Plan {
 constexpr int64_t kPastCache = int64_t(1) << 27;
 
 // The kernel and split with the least expected time, in us, by a model whose
-// constants were fitted to the times of all of them at 279 sizes (1 to 4096
-// tokens, weights of 128 x 256 to 28672 x 4096): its choice is within 0.7% of
-// the fastest on average, 26% at worst (1983 x 3220 x 256, where C's bytes
+// constants were fitted to the times of all of them at 280 sizes (1 to 3618
+// tokens, weights of 45 KB to 320 MB; profiles/int8_gemm_candidates.csv has the
+// times): its choice is within
+// 0.7% of the fastest on average, 26% at worst (1983 x 3220 x 256, where C's bytes
 // rule). Few tokens: a start, and for each round of 256 work-groups and 1024 k
 // a time that grows with M; two groups of 16 rows of B to each load of A where
 // that still gives most CUs a work-group (us, one group / two: 6144 x 4096, M = 4

@@ -1,13 +1,16 @@
 """Linear layers held in 8 bits: int8 codes with a scale for each token and
 each output channel, for layers and tokens that the MXFP4 products do not
-serve (any number of rows from one, any width).
+serve (any number of rows from one, widths that are no multiple of 32).
 
     codes, scales = int8_quantize(x)          one scale a row, a / 127
     c = int8_gemm(a, a_scales, b, b_scales)   (sum_k a b, exact) * scales
     y = int8_linear(x, w, w_scales)           both
 
 An operand is int8 [rows][pitch]: the pitch is the width rounded up to a
-multiple of 128, with zero codes past the width, which a product runs over.
+multiple of 128, with zero codes past the width, which a product runs over. (Codes
+of the width alone are taken too, by a kernel that is several times slower.)
+The quantizers take rows of up to 32768 columns, a product K up to 131071;
+wider calls raise.
 Inference only: a call in which an input, a scale or the bias requires a gradient
 is refused (torch.no_grad() or detached tensors). Marshalling only: every step
 runs in the library's kernels.
@@ -38,8 +41,8 @@ def int8_linear(x, w, w_scales, bias=None, out_dtype=None):
 
 def int8_mlp(x, norm_weight, eps, gate_up, gate_up_scales, down, down_scales, residual=None):
     """A feed-forward block in 8 bits: norm (of x + residual), gate and up
-    rows in one product (gate_up [2 F][K]: the gate's F rows first), silu(gate)
-    * up quantized in one pass, down product. Returns (y, h), h = x + residual
+    rows in one product (gate_up [2 F][K]: the gate's F rows first; its result
+    is held in x's type), silu(gate) * up quantized in one pass, down product. Returns (y, h), h = x + residual
     (x itself without a residual); the caller adds y to h, or hands both to
     the next block's norm."""
     return ops.int8_mlp(x, norm_weight, eps, gate_up, gate_up_scales, down, down_scales, residual)
