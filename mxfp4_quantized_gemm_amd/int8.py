@@ -68,12 +68,12 @@ class Int8Linear(torch.nn.Module):
     def from_weight(cls, weight, bias=None):
         """From a weight [out][in] in GPU memory (a Linear's or MXFP4Linear's) and
         its bias; both are copied."""
-        if bias is not None and bias.shape != weight.shape[:1]:
-            raise ValueError(f"bias must be [{weight.size(0)}], got {list(bias.shape)}")
+        if bias is not None and bias.numel() != weight.size(0):
+            raise ValueError(f"bias must hold {weight.size(0)} values, holds {bias.numel()}")
         layer = cls(weight.size(1), weight.size(0), bias is not None, weight.device)
         layer.weight, layer.scales = int8_quantize(weight.detach())
         if bias is not None:
-            layer.bias.copy_(bias)
+            layer.bias.copy_(bias.reshape(-1))
         return layer
 
     def _apply(self, fn, recurse=True):

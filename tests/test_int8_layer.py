@@ -56,3 +56,5 @@ def test_from_weight_copies_the_bias(monkeypatch):
             bias -= 1
     with pytest.raises(ValueError, match="bias"):
         int8.Int8Linear.from_weight(source.weight, torch.zeros(1))
+    # a bias of another shape, as the product takes it
+    assert torch.equal(int8.Int8Linear.from_weight(source.weight, want[None]).bias, want)
