@@ -985,7 +985,7 @@ struct Plan {
 constexpr int64_t kPastCache = int64_t(1) << 27;
 
 // The kernel and split with the least expected time, in us, by a model whose
-// constants were fitted to the times of all of them at 280 sizes (1 to 3618
+// constants were fitted to the times of all of them at 278 sizes (1 to 3618
 // tokens, weights of 45 KB to 320 MB; profiles/int8_gemm_candidates.csv has the
 // times): its choice is within
 // 0.7% of the fastest on average, 26% at worst (1983 x 3220 x 256, where C's bytes
