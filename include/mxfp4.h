@@ -437,6 +437,129 @@ int mxfp4_int8_gemm(const void* A, int64_t lda, const float* a_scales, const voi
                     hipStream_t stream);
 size_t mxfp4_int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/*
+ * ------------------------------------------------------------------------
+ * Attention's operators, between the query-key-value product and the output
+ * product of a block: the norm of each head of queries and keys with their
+ * rotation (with its gradient, in training), and for serving an int8 cache of
+ * keys and values in pages, written and read back, and the attention of one new
+ * token a sequence over it.
+ *
+ * Conventions beside those above: heads are [tokens][heads][dim] with any
+ * strides over tokens and heads (in elements, >= 0; also 0) and a unit stride
+ * in dim, 1 <= dim <= 256, heads <= 1024; results are dense and must not
+ * overlap the inputs. tokens (or batch) == 0 is a valid empty call.
+ */
+typedef struct {
+  const void* p;
+  int64_t heads, token_stride, head_stride;
+} mxfp4_heads;
+
+/* The rotation of a head's first 2 pairs values: pair p is (p, pairs + p), or
+ * (2 p, 2 p + 1) if interleaved, and turns by positions[axis][token]
+ * frequencies[p] radians, `axis` being that of p: axis_pairs[0] pairs of the
+ * first axis, then axis_pairs[1] of the second, ... The angle's product is taken in
+ * fp64. Values behind the pairs are not turned; pairs == 0: nothing is. */
+typedef struct {
+  const int64_t* positions;  /* [axes][tokens]                               */
+  const double* frequencies; /* [pairs]                                      */
+  int64_t pairs;             /* 0 <= 2 pairs <= dim                          */
+  int32_t axes;              /* 1 .. 4                                       */
+  int32_t interleaved;
+  int64_t axis_pairs[4];     /* those of the axes sum to pairs               */
+} mxfp4_rotation;
+
+/* A cache of int8 keys and values: codes k, v [pages][heads][page_size][pitch]
+ * (16-byte aligned), scales [pages][heads][page_size]. pitch is dim rounded up
+ * to a multiple of 64, page_size a multiple of 16, pages page_size < 2^31.
+ * A slot is a token's place, page page_size + (its row in the page). */
+typedef struct {
+  void* k;
+  float* k_scales;
+  void* v;
+  float* v_scales;
+  int64_t pages, heads, page_size, pitch;
+} mxfp4_int8_kv;
+
+/*
+ * mxfp4_qk_norm_rope -- for every head x of q and of k: u = x / sqrt(mean(x^2)
+ * + eps), z = u weight, and z turned by `rotation` (NULL: not), in fp32 (the mean
+ * in fp64, as mxfp4_rmsnorm), rounded to `dtype` once. eps < 0: no norm, then
+ * the weights are NULL. q_weight, k_weight [dim] of weight_dtype (`dtype` or
+ * fp32), NULL for 1. q_out [tokens][q heads][dim], k_out likewise. Either may
+ * have no heads.
+ */
+int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t tokens, int64_t dim,
+                       int dtype, const mxfp4_rotation* rotation, const void* q_weight,
+                       const void* k_weight, int weight_dtype, float eps, void* q_out, void* k_out,
+                       hipStream_t stream);
+
+/*
+ * mxfp4_qk_norm_rope_bwd -- gradients of mxfp4_qk_norm_rope. dq, dk: gradients
+ * of its outputs; q, k: its inputs. With dz = dy turned back and g = dz weight:
+ * dx = r (g - u mean(g u)) to dq_out and dk_out (dense, in `dtype`; without a
+ * norm dx = dz, and q and k are not read); dq_weight = sum over tokens and heads
+ * of dz u, dk_weight likewise, in weight_dtype (NULL: not wanted; both of them
+ * NULL without a norm; zeros where there are no tokens). Sums in fp32, in a
+ * fixed order. ws: mxfp4_qk_norm_rope_bwd_workspace_bytes bytes, 4-byte aligned
+ * (NULL where both weights' gradients are).
+ */
+int mxfp4_qk_norm_rope_bwd(const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* q,
+                           const mxfp4_heads* k, int64_t tokens, int64_t dim, int dtype,
+                           const mxfp4_rotation* rotation, const void* q_weight, const void* k_weight,
+                           int weight_dtype, float eps, void* dq_out, void* dk_out, void* dq_weight,
+                           void* dk_weight, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t mxfp4_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                              int64_t dim);
+
+/*
+ * mxfp4_int8_kv_write -- keys and values of new tokens into the cache: codes
+ * and scale of each head as mxfp4_int8_quantize makes them of a row, keys after
+ * norm and rotation as in mxfp4_qk_norm_rope, from their fp32 values (eps < 0 and
+ * rotation NULL: as they are). q (NULL: none) goes to q_out as there, in the same
+ * pass. slots [tokens]: where each token goes; a slot below 0 or outside the
+ * cache is not written. Of tokens with the same slot the last one stays. k and v
+ * have the cache's heads. Codes from dim to the pitch are set to 0; nothing else
+ * of the cache is touched.
+ */
+int mxfp4_int8_kv_write(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,
+                        int64_t tokens, int64_t dim, int dtype, const mxfp4_rotation* rotation,
+                        const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+                        const mxfp4_int8_kv* cache, const int64_t* slots, void* q_out,
+                        hipStream_t stream);
+
+/*
+ * mxfp4_int8_kv_read -- code times scale of the tokens at `slots`, rounded to
+ * `dtype`: k and v [tokens][heads][dim]. A slot outside the cache reads as 0.
+ */
+int mxfp4_int8_kv_read(const mxfp4_int8_kv* cache, const int64_t* slots, int64_t tokens, int64_t dim,
+                       int dtype, void* k, void* v, hipStream_t stream);
+
+/*
+ * mxfp4_paged_attention -- for each sequence b one token's queries q [batch]
+ * [heads][dim] (the "tokens" of mxfp4_heads are sequences) over its first n =
+ * lengths[b] cached tokens, the last `window` of them where window > 0. Token
+ * t is row t % page_size of page pages[b][t / page_size] (row pitch pages_ld,
+ * `table` columns). Query head h reads key head h / (q heads / cache heads);
+ * the quotient is whole. Scores scale (q . k), softmax, and the sum of values:
+ * out [batch][heads][dim] in `dtype`, lse [batch][heads] (NULL: not wanted) the
+ * logarithm of the sum of the scores' exponentials. A length below 0 counts as
+ * 0, one past the table as the table's end. A sequence with no token
+ * has out = 0 and lse = -infinity. Tokens of a page that is not in the cache
+ * (pages[b][i] < 0 or >= pages) do not count; nothing past the length or
+ * before the window does, whatever it holds. Sums in fp32; codes exact, queries
+ * exact, and the products of probabilities and scales held to 2^-16 (fp32: 2^-23).
+ * table page_size <= 2^31 - 1024. ws: mxfp4_paged_attention_workspace_bytes
+ * bytes, 4-byte aligned (may be 0, then ws may be NULL). Results do not depend on
+ * the order in which work-groups run.
+ */
+int mxfp4_paged_attention(const mxfp4_heads* q, int64_t batch, int64_t dim, int dtype,
+                          const mxfp4_int8_kv* cache, const int32_t* pages, int64_t pages_ld,
+                          int64_t table, const int32_t* lengths, float scale, int64_t window,
+                          void* out, float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t mxfp4_paged_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                             int64_t dim, int64_t table, int64_t page_size);
+
 /* Static text of a status code ("MXFP4_OK", ...); never NULL. */
 const char* mxfp4_status_string(int status);
 

@@ -35,9 +35,31 @@ EXPORTS = (
     "mxfp4_workspace_bytes", "mxfp4_status_string",
     "mxfp4_rmsnorm", "mxfp4_rmsnorm_int8", "mxfp4_rmsnorm_bwd", "mxfp4_rmsnorm_bwd_workspace_bytes",
     "mxfp4_int8_quantize", "mxfp4_int8_gemm", "mxfp4_int8_gemm_workspace_bytes",
+    "mxfp4_qk_norm_rope", "mxfp4_qk_norm_rope_bwd", "mxfp4_qk_norm_rope_bwd_workspace_bytes",
+    "mxfp4_int8_kv_write", "mxfp4_int8_kv_read", "mxfp4_paged_attention",
+    "mxfp4_paged_attention_workspace_bytes",
 )
 
 _LIB = None
+
+
+class Heads(ctypes.Structure):
+    """mxfp4_heads"""
+    _fields_ = [("p", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Rotation(ctypes.Structure):
+    """mxfp4_rotation"""
+    _fields_ = [("positions", ctypes.c_void_p), ("frequencies", ctypes.c_void_p), ("pairs", ctypes.c_int64),
+                ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("axis_pairs", ctypes.c_int64 * 4)]
+
+
+class Int8KV(ctypes.Structure):
+    """mxfp4_int8_kv"""
+    _fields_ = [("k", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("pitch", ctypes.c_int64)]
 
 
 class MXFP4Error(RuntimeError):
@@ -99,6 +121,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mxfp4_int8_gemm.restype = i32
     lib.mxfp4_int8_gemm_workspace_bytes.argtypes = [i64, i64, i64]
     lib.mxfp4_int8_gemm_workspace_bytes.restype = sz
+    heads, rot, kv = (ctypes.POINTER(t) for t in (Heads, Rotation, Int8KV))
+    lib.mxfp4_qk_norm_rope.argtypes = [heads, heads, i64, i64, i32, rot, p, p, i32, f32, p, p, p]
+    lib.mxfp4_qk_norm_rope.restype = i32
+    lib.mxfp4_qk_norm_rope_bwd.argtypes = [heads, heads, heads, heads, i64, i64, i32, rot, p, p, i32, f32, p, p, p,
+                                           p, p, sz, p]
+    lib.mxfp4_qk_norm_rope_bwd.restype = i32
+    lib.mxfp4_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.mxfp4_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    lib.mxfp4_int8_kv_write.argtypes = [heads, heads, heads, i64, i64, i32, rot, p, p, i32, f32, kv, p, p, p]
+    lib.mxfp4_int8_kv_write.restype = i32
+    lib.mxfp4_int8_kv_read.argtypes = [kv, p, i64, i64, i32, p, p, p]
+    lib.mxfp4_int8_kv_read.restype = i32
+    lib.mxfp4_paged_attention.argtypes = [heads, i64, i64, i32, kv, p, i64, i64, p, f32, i64, p, p, p, sz, p]
+    lib.mxfp4_paged_attention.restype = i32
+    lib.mxfp4_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
+    lib.mxfp4_paged_attention_workspace_bytes.restype = sz
     lib.mxfp4_status_string.argtypes = [i32]
     lib.mxfp4_status_string.restype = ctypes.c_char_p
     _LIB = lib
@@ -634,3 +672,163 @@ def mxfp4_int8_gemm(A, a_scales, B, b_scales, bias, C, ws, stream=None):
 
 def mxfp4_int8_gemm_workspace_bytes(M, N, K):
     return int(load_library().mxfp4_int8_gemm_workspace_bytes(M, N, K))
+
+
+# ------------------------------------------------- attention's C calls
+# Heads are 3-D tensors [tokens][heads][dim] with a unit stride in dim; a cache is
+# (k, k_scales, v, v_scales). rotary.py, kv_cache.py and attention.py allocate their
+# outputs and go through the binding in C++.
+def _heads(t, tokens, dim, dtype, name, device):
+    """mxfp4_heads of a tensor (None: no heads)."""
+    if t is None:
+        return Heads()
+    _on(t, device, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.size(0) != tokens or t.size(2) != dim:
+        raise ValueError(f"{name} must be [{tokens}][heads][{dim}], got {list(t.shape)}")
+    if t.stride(2) != 1 and dim > 1:
+        raise ValueError(f"{name} must have a unit stride in its last dimension")
+    return Heads(t.data_ptr(), t.size(1), t.stride(0) if tokens > 1 else 0, t.stride(1) if t.size(1) > 1 else 0)
+
+
+def _dense(t, shape, dtype, name, device):
+    """Address of an output of this shape (None: 0)."""
+    if t is None:
+        return 0
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _vec(t, t.numel(), dtype, name, device)
+
+
+def _out(x, t, name):
+    """Address of the output of the heads x (None: no heads)."""
+    if (x is None) != (t is None):
+        raise ValueError(f"{name} must be given where its heads are, and only there")
+    return 0 if x is None else _dense(t, x.shape, x.dtype, name, x.device)
+
+
+def _rotation(positions, frequencies, axis_pairs, interleaved, tokens, device):
+    """mxfp4_rotation (frequencies None: none)."""
+    import torch
+    if frequencies is None:
+        return Rotation(axes=1)
+    pairs = frequencies.numel()
+    axis_pairs = (pairs,) if axis_pairs is None else tuple(axis_pairs)
+    if not 1 <= len(axis_pairs) <= 4:
+        raise ValueError(f"axis_pairs must be 1 to 4 counts, got {list(axis_pairs)}")
+    return Rotation(_vec(positions, len(axis_pairs) * tokens, torch.int64, "positions", device),
+                    _vec(frequencies, pairs, torch.float64, "frequencies", device), pairs, len(axis_pairs),
+                    int(interleaved), (ctypes.c_int64 * 4)(*axis_pairs))
+
+
+def _head_weights(q_weight, k_weight, dim, dtype, device):
+    """Addresses of the weights, and their type."""
+    wt = dtype
+    for w in (q_weight, k_weight):
+        if w is not None:
+            wt = w.dtype
+            if w.numel() != dim:
+                raise ValueError(f"weights must hold {dim} values, one holds {w.numel()}")
+    return _vec(q_weight, dim, wt, "q_weight", device), _vec(k_weight, dim, wt, "k_weight", device), _dt(wt)
+
+
+def _kv(cache, device):
+    import torch
+    k, ks, v, vs = cache
+    for t, name in ((k, "cache k"), (v, "cache v")):
+        if t.dim() != 4 or t.shape != k.shape:
+            raise ValueError(f"{name} must be [pages][heads][page size][pitch], got {list(t.shape)}")
+    pages, heads, page, pitch = k.shape
+    i8, f32 = torch.int8, torch.float32
+    return Int8KV(_vec(k, k.numel(), i8, "cache k", device), _dense(ks, k.shape[:3], f32, "cache k_scales", device),
+                  _vec(v, k.numel(), i8, "cache v", device), _dense(vs, k.shape[:3], f32, "cache v_scales", device),
+                  pages, heads, page, pitch)
+
+
+def mxfp4_qk_norm_rope(q, k, positions, frequencies, q_weight, k_weight, eps, q_out, k_out, axis_pairs=None,
+                       interleaved=False, stream=None):
+    """Norm (eps below 0: none) and rotation (frequencies None: none) of q and k into q_out and k_out
+    (k and k_out may be None)."""
+    tokens, _, dim = q.shape
+    dtype, dev = q.dtype, q.device
+    args = (_heads(q, tokens, dim, dtype, "q", dev), _heads(k, tokens, dim, dtype, "k", dev), tokens, dim, _dt(dtype),
+            _rotation(positions, frequencies, axis_pairs, interleaved, tokens, dev),
+            *_head_weights(q_weight, k_weight, dim, dtype, dev), eps, _out(q, q_out, "q_out"), _out(k, k_out, "k_out"))
+    _run(load_library().mxfp4_qk_norm_rope, args, dev, stream)
+
+
+def mxfp4_qk_norm_rope_bwd(dq, dk, q, k, positions, frequencies, q_weight, k_weight, eps, dq_out, dk_out, dq_weight,
+                           dk_weight, ws, axis_pairs=None, interleaved=False, stream=None):
+    """Gradients of mxfp4_qk_norm_rope (the weights' and ws may be None; dk, k and dk_out too)."""
+    import torch
+    tokens, _, dim = q.shape
+    dtype, dev = q.dtype, q.device
+    qw, kw, wt = _head_weights(q_weight, k_weight, dim, dtype, dev)
+    grads = [t for t in (dq_weight, dk_weight) if t is not None]
+    if q_weight is None and k_weight is None and grads:
+        wt = _dt(grads[0].dtype)
+    type_of = {v: t for t, v in _DT.items()}[wt]
+    if (dk is None) != (k is None) or (k is not None and dk.shape != k.shape) or dq.shape != q.shape:
+        raise ValueError("dq and dk must have the shapes of q and k")
+    args = (_heads(dq, tokens, dim, dtype, "dq", dev), _heads(dk, tokens, dim, dtype, "dk", dev),
+            _heads(q, tokens, dim, dtype, "q", dev), _heads(k, tokens, dim, dtype, "k", dev), tokens, dim, _dt(dtype),
+            _rotation(positions, frequencies, axis_pairs, interleaved, tokens, dev), qw, kw, wt, eps,
+            _out(q, dq_out, "dq_out"), _out(k, dk_out, "dk_out"),
+            _dense(dq_weight, (dim,), type_of, "dq_weight", dev), _dense(dk_weight, (dim,), type_of, "dk_weight", dev),
+            _vec(ws, 0, torch.uint8, "ws", dev), 0 if ws is None else ws.numel())
+    _run(load_library().mxfp4_qk_norm_rope_bwd, args, dev, stream)
+
+
+def mxfp4_qk_norm_rope_bwd_workspace_bytes(tokens, q_heads, k_heads, dim):
+    return int(load_library().mxfp4_qk_norm_rope_bwd_workspace_bytes(tokens, q_heads, k_heads, dim))
+
+
+def mxfp4_int8_kv_write(q, k, v, positions, frequencies, q_weight, k_weight, eps, cache, slots, q_out,
+                        axis_pairs=None, interleaved=False, stream=None):
+    """Keys and values into the cache, queries to q_out (q and q_out may be None; norm and rotation
+    as in mxfp4_qk_norm_rope)."""
+    import torch
+    tokens, _, dim = k.shape
+    dtype, dev = k.dtype, k.device
+    args = (_heads(q, tokens, dim, dtype, "q", dev), _heads(k, tokens, dim, dtype, "k", dev),
+            _heads(v, tokens, dim, dtype, "v", dev), tokens, dim, _dt(dtype),
+            _rotation(positions, frequencies, axis_pairs, interleaved, tokens, dev),
+            *_head_weights(q_weight, k_weight, dim, dtype, dev), eps, _kv(cache, dev),
+            _vec(slots, tokens, torch.int64, "slots", dev), _out(q, q_out, "q_out"))
+    _run(load_library().mxfp4_int8_kv_write, args, dev, stream)
+
+
+def mxfp4_int8_kv_read(cache, slots, k, v, stream=None):
+    """Code times scale of the tokens at slots into k and v [tokens][heads][dim]."""
+    import torch
+    tokens, heads, dim = k.shape
+    dev = k.device
+    kv = _kv(cache, dev)
+    if heads != kv.heads:
+        raise ValueError(f"k must have the cache's {kv.heads} heads, got {list(k.shape)}")
+    args = (kv, _vec(slots, tokens, torch.int64, "slots", dev), tokens, dim, _dt(k.dtype),
+            _dense(k, k.shape, k.dtype, "k", dev), _dense(v, k.shape, k.dtype, "v", dev))
+    _run(load_library().mxfp4_int8_kv_read, args, dev, stream)
+
+
+def mxfp4_paged_attention(q, cache, pages, lengths, scale, window, out, lse, ws, stream=None):
+    """Attention of q [batch][heads][dim] over the cache (lse and ws may be None)."""
+    import torch
+    batch, heads, dim = q.shape
+    dtype, dev = q.dtype, q.device
+    _on(pages, dev, "pages")
+    if pages.dtype is not torch.int32 or pages.dim() != 2 or pages.size(0) != batch:
+        raise ValueError(f"pages must be int32 [{batch}][pages of a sequence], got {pages.dtype} {list(pages.shape)}")
+    if pages.stride(1) != 1 and pages.size(1) > 1:
+        raise ValueError("pages must have a unit column stride")
+    args = (_heads(q, batch, dim, dtype, "q", dev), batch, dim, _dt(dtype), _kv(cache, dev), pages.data_ptr(),
+            pages.stride(0) if batch > 1 else pages.size(1), pages.size(1),
+            _vec(lengths, batch, torch.int32, "lengths", dev), scale, window,
+            _dense(out, q.shape, dtype, "out", dev), _dense(lse, q.shape[:2], torch.float32, "lse", dev),
+            0 if ws is None else _vec(ws, 0, torch.uint8, "ws", dev), 0 if ws is None else ws.numel())
+    _run(load_library().mxfp4_paged_attention, args, dev, stream)
+
+
+def mxfp4_paged_attention_workspace_bytes(batch, q_heads, kv_heads, dim, table, page_size):
+    return int(load_library().mxfp4_paged_attention_workspace_bytes(batch, q_heads, kv_heads, dim, table, page_size))

@@ -1,4 +1,4 @@
-"""The torch binding of the norm and 8-bit operators. Without it they raise:
+"""The torch binding of the norm, 8-bit and attention operators. Without it they raise:
 there is no fallback."""
 import torch  # noqa: F401  (its libraries come first)
 

@@ -1,5 +1,5 @@
 """Build libmxfp4.so (gfx950) in-tree with hipcc, and the torch binding of the
-norm and 8-bit operators (_ops.so, host code only) with g++.
+norm, 8-bit and attention operators (_ops.so, host code only) with g++.
 
 Usage: python -m mxfp4_quantized_gemm_amd.build  (or build() from Python).
 Every HIP source is compiled with -ffp-contract=off (the rotation butterfly
@@ -21,8 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp4.so")
 OPS = os.path.join(PKG, "_ops.so")
-SOURCES = ["api.cpp", "api_int8.cpp", "quant.hip", "gemm.hip", "stats.hip", "norm.hip",
-           "int8_gemm.hip"]
+SOURCES = ["api.cpp", "api_int8.cpp", "api_attention.cpp", "quant.hip", "gemm.hip", "stats.hip", "norm.hip",
+           "int8_gemm.hip", "heads.hip", "attention.hip"]
+OPS_SOURCES = ["torch_ops.cpp", "torch_attention.cpp"]
 ARCH = "gfx950"
 
 
@@ -75,24 +76,29 @@ def _no_ops() -> str | None:
     return None
 
 
-def _compile_ops() -> str:
-    """torch_ops.cpp -> object: host code against torch's and HIP's headers."""
+def _compile_ops() -> list[str]:
+    """OPS_SOURCES -> objects: host code against torch's and HIP's headers."""
+    with cf.ThreadPoolExecutor(max_workers=len(OPS_SOURCES)) as ex:
+        return list(ex.map(_compile_ops_source, OPS_SOURCES))
+
+
+def _compile_ops_source(src: str) -> str:
     import torch
     from torch.utils import cpp_extension
-    out = os.path.join(BUILD, "torch_ops.cpp.o")
+    out = os.path.join(BUILD, src + ".o")
     _run([shutil.which("g++"), "-O2", "-std=c++17", "-fPIC", "-c", "-D__HIP_PLATFORM_AMD__",
           "-DUSE_ROCM", "-DTORCH_EXTENSION_NAME=_ops", "-DTORCH_API_INCLUDE_EXTENSION_H",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *(f for d in [*cpp_extension.include_paths(), os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
                         sysconfig.get_paths()["include"]] for f in ("-isystem", d)),
-          os.path.join(CSRC, "torch_ops.cpp"), "-o", out], "g++ on torch_ops.cpp")
+          os.path.join(CSRC, src), "-o", out], f"g++ on {src}")
     return out
 
 
-def _link_ops(obj: str) -> None:
+def _link_ops(objs) -> None:
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    _run([shutil.which("g++"), "-shared", "-o", OPS + ".tmp", obj, "-L" + PKG, "-l:libmxfp4.so",
+    _run([shutil.which("g++"), "-shared", "-o", OPS + ".tmp", *objs, "-L" + PKG, "-l:libmxfp4.so",
           "-L" + libs, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch", "-ltorch_python",
           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs], "linking _ops.so")
     os.replace(OPS + ".tmp", OPS)
@@ -108,7 +114,7 @@ def build(verbose: bool = False) -> str:
     """Compile every source and link both libraries; returns libmxfp4.so's path.
 
     libmxfp4.so is linked first and needs nothing of the torch binding; on a
-    machine without g++ or torch's headers it is built alone (the norm and 8-bit
+    machine without g++ or torch's headers it is built alone (the norm, 8-bit and attention
     modules then raise when they are imported)."""
     os.makedirs(BUILD, exist_ok=True)
     lacking = _no_ops()
@@ -118,7 +124,7 @@ def build(verbose: bool = False) -> str:
         if ops:
             _link_ops(ops.result())
     if lacking:
-        sys.stderr.write(f"_ops.so (norm and 8-bit operators from Python) is not built: {lacking}\n")
+        sys.stderr.write(f"_ops.so (norm, 8-bit and attention operators from Python) is not built: {lacking}\n")
         if os.path.exists(OPS):  # it may not fit the new library
             os.remove(OPS)
     if verbose:

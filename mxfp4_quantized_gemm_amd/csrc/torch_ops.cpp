@@ -4,107 +4,10 @@
 // computes nothing itself. These operators run once per layer and token when
 // one token is decoded, and take a few microseconds on the GPU then; a binding
 // in Python (ctypes) cost 8 us a call and the norm's gradient 135 us.
-#include <c10/core/DeviceGuard.h>
-#include <c10/hip/HIPStream.h>
-#include <torch/csrc/jit/frontend/tracer.h>
-#include <torch/extension.h>
+#include "torch_common.h"
 
-#include <optional>
-#include <tuple>
-
-#include "../../include/mxfp4.h"
-
+namespace mx {
 namespace {
-
-using at::Tensor;
-using torch::autograd::AutogradContext;
-using torch::autograd::variable_list;
-typedef std::optional<Tensor> Maybe;
-
-int dtype_of(const Tensor& t, const char* name) {
-  const auto s = t.scalar_type();
-  TORCH_CHECK_TYPE(s == at::kFloat || s == at::kBFloat16 || s == at::kHalf, name,
-                   " must be float32, bfloat16 or float16, got ", s);
-  return s == at::kFloat ? MXFP4_DT_F32 : s == at::kBFloat16 ? MXFP4_DT_BF16 : MXFP4_DT_F16;
-}
-
-// Raises the package's MXFP4Error for a status other than MXFP4_OK. The GIL is held.
-void check(int status, const char* where) {
-  if (status == MXFP4_OK) return;
-  const py::object cls = py::module_::import("mxfp4_quantized_gemm_amd").attr("MXFP4Error");
-  const py::object e = cls(status, where);
-  PyErr_SetObject(cls.ptr(), e.ptr());
-  throw py::error_already_set();
-}
-
-// torch.jit.trace would record the outputs' allocation alone: replays of it would
-// return memory that nothing wrote.
-void no_trace(const char* where) {
-  TORCH_CHECK(!torch::jit::tracer::isTracing(), where, " cannot be recorded by torch.jit.trace");
-}
-
-// A forward-mode tangent of an input would be dropped, which is a derivative of
-// zero. (no_grad() does not switch forward mode off.)
-void no_tangent(const char* where, std::initializer_list<const Tensor*> inputs) {
-  for (const Tensor* t : inputs)
-    TORCH_CHECK(t == nullptr || !t->defined() || !t->_fw_grad(0).defined(), where,
-                " has no forward-mode derivative");
-}
-
-// Codes and their products have no gradient, in their scales and bias neither:
-// a call that autograd would have to record is refused.
-void no_gradient(const char* where, std::initializer_list<const Tensor*> inputs) {
-  no_trace(where);
-  no_tangent(where, inputs);
-  if (!at::GradMode::is_enabled()) return;
-  for (const Tensor* t : inputs)
-    TORCH_CHECK(t == nullptr || !t->requires_grad(), where,
-                " has no gradient: call it under torch.no_grad() or on detached tensors");
-}
-
-hipStream_t stream_of(const Tensor& t) { return c10::hip::getCurrentHIPStream(t.device().index()).stream(); }
-
-bool has(const Maybe& t) { return t.has_value() && t->defined(); }
-const Tensor* ptr(const Maybe& t) { return has(t) ? &*t : nullptr; }
-
-void on_gpu(const Tensor& t, const char* name, const Tensor* like = nullptr) {
-  TORCH_CHECK_VALUE(t.is_cuda(), name, " must live in GPU memory");
-  TORCH_CHECK_VALUE(like == nullptr || t.device() == like->device(), name, " must be on ",
-                    like ? like->device() : t.device(), ", is on ", t.device());
-}
-
-// t [..., cols] as [rows][cols] with a unit column stride and rows that do not
-// overlap: a view where it has them, a copy where not.
-struct Rows {
-  Tensor t;
-  int64_t rows, cols, ld;
-  const void* p() const { return t.const_data_ptr(); }
-};
-
-Rows rows_of(const Tensor& t, const char* name) {
-  TORCH_CHECK_VALUE(t.dim() >= 1, name, " must have a dimension");
-  Rows r{t, 0, t.size(-1), 0};
-  if (t.dim() != 2) {
-    int64_t n = 1;
-    for (int64_t i = 0; i + 1 < t.dim(); ++i) n *= t.size(i);
-    r.t = t.reshape({n, r.cols});
-  }
-  r.rows = r.t.size(0);
-  if ((r.t.stride(1) != 1 && r.cols > 1) || (r.t.stride(0) < r.cols && r.rows > 1))
-    r.t = r.t.clone(at::MemoryFormat::Contiguous);
-  r.ld = r.rows > 1 ? r.t.stride(0) : r.cols;
-  return r;
-}
-
-const float* floats(const Tensor& t, int64_t n, const char* name, const Tensor& like) {
-  on_gpu(t, name, &like);
-  TORCH_CHECK_TYPE(t.scalar_type() == at::kFloat, name, " must be float32, got ", t.scalar_type());
-  TORCH_CHECK_VALUE(t.numel() == n && t.is_contiguous(), name, " must hold ", n, " contiguous values, holds ",
-                    t.numel());
-  return t.const_data_ptr<float>();
-}
-
-int64_t padded(int64_t cols) { return (cols + 127) / 128 * 128; }
 
 // ------------------------------------------------------------------ norm
 // x, residual and weight of a norm, checked.
@@ -224,14 +127,12 @@ py::object rms_norm(const Tensor& x, const Maybe& weight, double eps, const Mayb
   return o.h.defined() ? py::object(py::make_tuple(o.y, o.h)) : py::cast(o.y);
 }
 
-struct Operand {
-  Tensor codes, scales;
-};
-
 Operand new_operand(const Rows& x) {
   return {at::empty({x.rows, padded(x.cols)}, x.t.options().dtype(at::kChar)),
           at::empty({x.rows}, x.t.options().dtype(at::kFloat))};
 }
+
+}  // namespace
 
 Operand norm_int8(const Tensor& x, const Maybe& weight, double eps, const Maybe& residual, Tensor* h) {
   no_gradient("rms_norm_int8", {&x, ptr(weight), ptr(residual)});
@@ -246,11 +147,15 @@ Operand norm_int8(const Tensor& x, const Maybe& weight, double eps, const Maybe&
   return o;
 }
 
+namespace {
+
 py::tuple rms_norm_int8(const Tensor& x, const Maybe& weight, double eps, const Maybe& residual) {
   Tensor h;
   const Operand o = norm_int8(x, weight, eps, residual, &h);
   return h.defined() ? py::make_tuple(o.codes, o.scales, h) : py::make_tuple(o.codes, o.scales);
 }
+
+}  // namespace
 
 // ------------------------------------------------------------ 8 bits
 Operand quantize(const Tensor& x, const Maybe& gate) {
@@ -274,6 +179,8 @@ Operand quantize(const Tensor& x, const Maybe& gate) {
         "mxfp4_int8_quantize");
   return o;
 }
+
+namespace {
 
 py::tuple int8_quantize(const Tensor& x, const Maybe& gate) {
   const Operand o = quantize(x, gate);
@@ -319,6 +226,8 @@ Tensor int8_gemm(const Tensor& a, const Tensor& sa, const Tensor& b, const Tenso
   return gemm(a, sa, b, sb, bias, a.size(1), out);
 }
 
+}  // namespace
+
 // The product of quantized rows with a weight that is padded as they are (then
 // over the zero codes too), or that has just the rows' own columns.
 Tensor product(const Operand& x, const Tensor& w, const Tensor& sw, const Maybe& bias, at::ScalarType out) {
@@ -330,12 +239,14 @@ void check_weight(const Tensor& w, int64_t cols, const char* name) {
                     " or ", padded(cols), " columns, got ", w.sizes());
 }
 
-Tensor as(const Tensor& y, const Tensor& x) {  // y [rows][N] with x's leading dimensions
+Tensor as(const Tensor& y, const Tensor& x) {
   if (x.dim() == 2) return y;
   auto s = x.sizes().vec();
   s.back() = y.size(1);
   return y.view(s);
 }
+
+namespace {
 
 Tensor int8_linear(const Tensor& x, const Tensor& w, const Tensor& sw, const Maybe& bias,
                    std::optional<at::ScalarType> out) {
@@ -363,9 +274,11 @@ py::tuple int8_mlp(const Tensor& x, const Maybe& weight, double eps, const Tenso
 }
 
 }  // namespace
+}  // namespace mx
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   namespace p = pybind11;
+  using namespace mx;
   m.def("rms_norm", &rms_norm, p::arg("x"), p::arg("weight"), p::arg("eps"), p::arg("residual"));
   m.def("rms_norm_int8", &rms_norm_int8, p::arg("x"), p::arg("weight"), p::arg("eps"), p::arg("residual"));
   m.def("int8_quantize", &int8_quantize, p::arg("x"), p::arg("gate"));
@@ -375,4 +288,5 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
         p::arg("out_dtype"));
   m.def("int8_mlp", &int8_mlp, p::arg("x"), p::arg("norm_weight"), p::arg("eps"), p::arg("gate_up"),
         p::arg("gate_up_scales"), p::arg("down"), p::arg("down_scales"), p::arg("residual"));
+  bind_attention(m);
 }

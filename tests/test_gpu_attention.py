@@ -1,0 +1,384 @@
+"""Attention of one new token a sequence over the paged int8 cache against a plain
+implementation in 64 bits (attention_util.attend64 has the tolerance), and the
+8-bit block against its parts."""
+import pytest
+import torch
+
+from tests.attention_util import TYPES, U, attend64, frequencies, half_step, make_cache, make_tables, near, rand
+
+pytestmark = pytest.mark.gpu
+PARTS = {"bf16": 2.0 ** -16, "fp16": 2.0 ** -16, "fp32": 3 * U}
+
+
+def case(lengths, H, K, D, page, dtype, seed, size=2.0, spare=2):
+    need = sum((n + page - 1) // page for n in lengths if n > 0)
+    cache = make_cache(need + spare, K, page, D, seed)
+    table = make_tables([max(n, 0) for n in lengths], page, need + spare, seed)
+    return dict(q=rand((len(lengths), H, D), TYPES[dtype], seed, size), cache=cache, table=table, lengths=lengths,
+                dtype=dtype)
+
+
+def run(c, q=None, scale=None, window=0, return_lse=True):
+    from mxfp4_quantized_gemm_amd.attention import paged_attention
+    return paged_attention(c["q"].cuda() if q is None else q, [t.cuda() for t in c["cache"]], c["table"].cuda(),
+                           torch.tensor(c["lengths"], dtype=torch.int32).cuda(), scale, window, return_lse)
+
+
+def check(c, scale=None, window=0):
+    D, dt = c["q"].shape[2], TYPES[c["dtype"]]
+    o, lse, tol = attend64(c["q"], c["cache"], c["table"], c["lengths"], D ** -0.5 if scale is None else scale, window,
+                           dt, PARTS[c["dtype"]])
+    got, got_lse = run(c, scale=scale, window=window)
+    assert got.dtype == dt
+    near(got, o, tol + half_step(o, dt), "o")
+    some = lse.isfinite()
+    assert torch.equal(got_lse.cpu()[~some].double(), lse[~some])
+    # relative errors of the sum are absolute ones of its logarithm: the scores' and the sum's,
+    # as in tol, with sum |q| |k| below dim * 8 * 8; and its own roundings
+    n = max(c["lengths"])
+    near(got_lse.cpu()[some], lse[some], ((D + 16) * U * D * 64 * D ** -0.5 + (n + 64) * U) * torch.ones_like(lse[some])
+         + 8 * U * lse[some].abs(), "lse")
+
+
+# head widths and layouts, up to several tiles of query heads
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("H,K,D", [(1, 1, 1), (4, 4, 8), (3, 1, 33), (32, 8, 128), (8, 2, 64), (14, 2, 80), (5, 1, 111),
+                                   (16, 1, 128), (17, 1, 64), (40, 1, 64), (6, 3, 130), (2, 2, 192), (12, 1, 256)])
+def test_layouts(H, K, D, dtype):
+    check(case([1, 37, 300], H, K, D, 16, dtype, H + D))
+
+
+# lengths around the tiles, units and pages; empty ones; pages that end inside a tile
+@pytest.mark.parametrize("page", [16, 48, 64, 256])
+def test_lengths(page):
+    lengths = [0, 1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 127, 128, 129, 255, 256, 257, 0, 511, 513, 1000]
+    check(case(lengths, 4, 2, 64, page, "fp32", page))
+    check(case(lengths, 4, 2, 128, page, "bf16", page + 1))
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 128, 129, 1000, 1 << 40])
+def test_window(window):
+    check(case([0, 1, 5, 16, 40, 129, 130, 700, 1001], 4, 1, 64, 16, "fp32", window % 997), window=window)
+
+
+@pytest.mark.parametrize("lengths", [[9000], [70001, 3, 0, 500], [20] * 700, [0] * 5, list(range(1, 400, 3)),
+                                     [1] * 1500 + [4000, 0, 130]])
+def test_shares(lengths):
+    """Lines cut over many work-groups, several in one, more sequences than a launch takes."""
+    check(case(lengths, 2, 1, 64, 64, "fp32", len(lengths)))
+    check(case(lengths, 6, 2, 64, 16, "bf16", len(lengths) + 1))
+
+
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, 30.0])
+def test_scale(scale):
+    """Flat, peaked (one token has all) and turned scores."""
+    check(case([200, 1, 77], 4, 2, 64, 16, "fp32", 3, size=0.5), scale=scale)
+
+
+def test_scores_that_grow_and_fall():
+    """The running maximum rises at every tile, or only at the first."""
+    for order in (1, -1):
+        c = case([900], 4, 1, 64, 64, "fp32", 4)
+        c["table"] = torch.arange(15, dtype=torch.int32)[None]
+        s = order * torch.linspace(-1, 1, 900)
+        c["cache"][0][..., :] = 0
+        c["cache"][0][..., 0] = 100
+        c["q"][:] = 0
+        c["q"][..., 0] = 50
+        c["cache"][1].view(-1)[:900] = s / 100
+        check(c, scale=1.0)
+
+
+def test_nothing_but_the_sequence_counts():
+    """NaN and infinities behind the length, before the window, in pages that no table has, and in the codes'
+    columns past the width."""
+    c = case([100, 0, 37, 300], 4, 2, 80, 16, "bf16", 5)
+    want = run(c, window=64)
+    k, ks, v, vs = c["cache"]
+    used = torch.zeros(k.shape[0], 16, dtype=torch.bool)
+    for b, n in enumerate(c["lengths"]):
+        t = torch.arange(max(0, n - 64), n)
+        used[c["table"][b].long()[t // 16], t % 16] = True
+    bad = ~used[:, None, :].expand(-1, 2, -1)
+    for i, x in enumerate((float("nan"), float("inf"), -float("inf"), 3e38)):
+        ks[bad], vs[bad] = x, x
+        k[..., 80:], v[..., 80:] = 100 + i, -100
+        got = run(c, window=64)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), x
+
+
+def test_pages_that_are_not_in_the_cache():
+    """Their tokens do not count; a sequence with none else gives zeros."""
+    c = case([200, 64, 100], 4, 2, 64, 16, "fp32", 6)
+    c["table"][0, 3], c["table"][0, 12], c["table"][0, 0] = -1, c["cache"][0].shape[0], 1 << 30
+    c["table"][1, :] = -(1 << 31)
+    check(c)
+    o, lse = run(c)
+    assert not o[1].any() and (lse[1] == -float("inf")).all()
+
+
+def test_lengths_past_the_table_and_below_zero():
+    c = case([64, 40, 0], 4, 2, 64, 16, "fp32", 7)
+    c["table"] = c["table"][:, :4]
+    full = run(c)
+    c["lengths"] = [1 << 30, 40, -7]
+    got = run(c)
+    assert torch.equal(got[0], full[0]) and torch.equal(got[1], full[1])
+
+
+def test_no_table():
+    c = case([0, 0], 4, 2, 64, 16, "bf16", 8)
+    c["table"], c["lengths"] = c["table"][:, :0], [5, 0]
+    o, lse = run(c)
+    assert not o.any() and (lse == -float("inf")).all()
+    c = case([], 4, 2, 64, 16, "bf16", 8)
+    assert run(c)[0].shape == (0, 4, 64)
+
+
+def test_not_finite_where_it_counts():
+    """A NaN or infinite scale, or query, reaches its own rows and no others."""
+    c = case([100, 60], 4, 2, 64, 16, "bf16", 9)
+    want, _ = run(c)
+    page = int(c["table"][0, 2])
+    c["cache"][3][page, 1, 5] = float("nan")
+    got, _ = run(c)
+    assert got[0, 2:].isnan().all() and torch.equal(got[0, :2], want[0, :2]) and torch.equal(got[1], want[1])
+    c["cache"][3][page, 1, 5] = 1.0
+    c["cache"][1][page, 1, 5] = float("nan")
+    got, _ = run(c)
+    assert got[0, 2:].isnan().all() and torch.equal(got[0, :2], want[0, :2]) and torch.equal(got[1], want[1])
+    c["cache"][1][page, 1, 5] = 1.0
+    for dtype in TYPES:
+        d = dict(c, q=c["q"].to(TYPES[dtype]), dtype=dtype)
+        want, _ = run(d)
+        for x in (float("nan"), float("inf")):
+            d["q"] = c["q"].to(TYPES[dtype]).clone()
+            d["q"][1, 1, 7] = x
+            got, _ = run(d)
+            assert got[1, 1].isnan().all()
+            got[1, 1] = want[1, 1]
+            assert torch.equal(got, want)
+    # an infinite query beside codes of one sign: all scores the same infinity
+    for dtype in TYPES:
+        d = case([50], 1, 1, 64, 16, dtype, 10)
+        d["cache"][0][:] = d["cache"][0].abs().clamp(min=1)
+        d["q"][0, 0, 3] = -float("inf")
+        o, lse = run(d)
+        assert (lse == -float("inf")).all() and not o.any()
+
+
+def test_one_token():
+    """Its value, whatever the score: one over itself."""
+    for dtype in TYPES:
+        c = case([1], 8, 2, 128, 16, dtype, 11, size=30.0)
+        o, _ = run(c)
+        _, _, v, vs = c["cache"]
+        p = int(c["table"][0, 0])
+        ref = (v[p, :, 0].double() * vs[p, :, 0].double()[:, None]).repeat_interleave(4, 0)[None]
+        near(o, ref, half_step(ref, TYPES[dtype]) + PARTS[dtype] * ref.abs() + 4 * U * ref.abs(), "o")
+
+
+def test_strides():
+    c = case([70, 200], 4, 2, 64, 16, "bf16", 12)
+    want = run(c)
+    q = c["q"].cuda()
+    wide = torch.cat([q, q + 1, q], 1)[:, :4]
+    back = q.transpose(0, 1).contiguous().transpose(0, 1)
+    last = torch.stack([q, q], -1)[..., 1]
+    odd = torch.empty(2 * 4 * 67 + 3, dtype=q.dtype, device="cuda")[3:].view(2, 4, 67)[..., 2:66]
+    odd.copy_(q)
+    for t in (wide, back, last, odd):
+        got = run(c, q=t)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    d = dict(c, table=torch.cat([c["table"]] * 2, 1)[:, : c["table"].shape[1]])  # rows of a wider table
+    assert torch.equal(run(d)[0], want[0])
+    d = dict(c, table=c["table"].t().contiguous().t())
+    assert torch.equal(run(d)[0], want[0])
+    d = dict(c, lengths=[70, 70], q=c["q"][:1].expand(2, -1, -1), table=c["table"][:1].expand(2, -1))
+    o, _ = run(d)
+    assert torch.equal(o[0], o[1])
+
+
+def test_deterministic_and_alone():
+    """The same bits again; without lse the same output."""
+    c = case([5000, 3, 900], 8, 2, 128, 64, "bf16", 13)
+    a, b = run(c), run(c)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(run(c, return_lse=False), a[0])
+
+
+def test_offsets_past_32_bits():
+    """Pages on both sides of byte 2^32 of the codes."""
+    from mxfp4_quantized_gemm_amd.attention import paged_attention
+    small = make_cache(4, 8, 64, 128, 14)
+    pages = (1 << 32) // (8 * 64 * 128) + 2
+    where = torch.tensor([0, pages - 1, pages - 2, pages - 3])
+    big = [torch.zeros(pages, *t.shape[1:], dtype=t.dtype, device="cuda") for t in small]
+    for t, s in zip(big, small):
+        t[where.cuda()] = s.cuda()
+    q, n = rand((1, 16, 128), torch.bfloat16, 14).cuda(), torch.tensor([250], dtype=torch.int32).cuda()
+    a = paged_attention(q, [t.cuda() for t in small], torch.arange(4, dtype=torch.int32)[None].cuda(), n)
+    assert torch.equal(paged_attention(q, big, where.int()[None].cuda(), n), a)
+
+
+def test_two_streams_at_once():
+    c, d = case([3000, 10], 4, 2, 64, 16, "bf16", 15), case([4000, 50], 4, 2, 64, 16, "bf16", 16)
+    want = [run(x)[0] for x in (c, d)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for x, s in zip((c, d), streams):
+        with torch.cuda.stream(s):
+            got.append(run(x)[0])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_c_entry_point():
+    import mxfp4_quantized_gemm_amd as mx
+    c = case([3000, 0, 130], 8, 2, 80, 16, "fp16", 17)
+    want, lse = run(c, scale=0.1, window=900)
+    q, cache, table = c["q"].cuda(), [t.cuda() for t in c["cache"]], c["table"].cuda()
+    n = torch.tensor(c["lengths"], dtype=torch.int32).cuda()
+    out, l = torch.empty_like(q), torch.empty(3, 8, device="cuda")
+    ws = torch.empty(mx.mxfp4_paged_attention_workspace_bytes(3, 8, 2, 80, table.shape[1], 16), dtype=torch.uint8,
+                     device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    mx.mxfp4_paged_attention(q, cache, table, n, 0.1, 900, out, l, ws, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(l, lse)
+    with pytest.raises(mx.MXFP4Error, match="WORKSPACE"):
+        mx.mxfp4_paged_attention(q, cache, table, n, 0.1, 900, out, l, ws[:-1])
+
+
+# -------------------------------------------------- the block, and a run together
+def block(K, H, KV, D, seed, dtype=torch.bfloat16):
+    from mxfp4_quantized_gemm_amd.int8 import int8_quantize
+    w = dict(norm=(1 + 0.1 * rand((K,), torch.float32, seed)).to(dtype).cuda())
+    w["qkv"] = int8_quantize(rand(((H + 2 * KV) * D, K), dtype, seed + 1, K ** -0.5).cuda())
+    w["out"] = int8_quantize(rand((K, H * D), dtype, seed + 2, (H * D) ** -0.5).cuda())
+    w["qw"], w["kw"] = ((1 + 0.1 * rand((D,), torch.float32, seed + i)).to(dtype).cuda() for i in (3, 4))
+    return w
+
+
+def step(w, x, res, cache, slots, table, n, pos, freq, D, **kw):
+    from mxfp4_quantized_gemm_amd.attention import int8_attention
+    return int8_attention(x, w["norm"], 1e-5, *w["qkv"], *w["out"], cache, slots, table, n, pos, freq, w["qw"], w["kw"],
+                          1e-6, head_dim=D, residual=res, **kw)
+
+
+def parts(w, x, res, cache, slots, table, n, pos, freq, D, window=0, **kw):
+    """The block by the public calls that it stands for."""
+    from mxfp4_quantized_gemm_amd.attention import paged_attention
+    from mxfp4_quantized_gemm_amd.int8 import int8_gemm, int8_linear
+    from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_append
+    from mxfp4_quantized_gemm_amd.norm import rms_norm_int8
+    K = x.shape[-1]
+    KV = cache[0].shape[1]
+    o = rms_norm_int8(x, w["norm"], 1e-5, residual=res)
+    h = o[2] if res is not None else x
+    mid = int8_gemm(o[0], o[1], *w["qkv"], out_dtype=x.dtype)
+    heads = mid.view(mid.shape[0], -1, D)
+    q, k, v = heads.split([heads.shape[1] - 2 * KV, KV, KV], 1)
+    q = int8_kv_append(q, k, v, cache, slots.reshape(-1), pos.reshape(*pos.shape[: pos.dim() - slots.dim()], -1), freq,
+                       w["qw"], w["kw"], 1e-6, **kw)
+    a = paged_attention(q, cache, table, n, window=window)
+    return int8_linear(a.reshape(a.shape[0], -1), *w["out"]).reshape(x.shape), h
+
+
+@pytest.mark.parametrize("H,KV,D,K,res", [(4, 2, 64, 256, True), (8, 1, 80, 200, False), (3, 3, 128, 512, True)])
+def test_block_is_its_parts(H, KV, D, K, res):
+    from mxfp4_quantized_gemm_amd.kv_cache import Int8KVCache
+    w, B = block(K, H, KV, D, H), 5
+    lengths = [1, 33, 130, 500, 64]
+    cache = [t.cuda() for t in make_cache(60, KV, 16, D, 1)]
+    table = make_tables(lengths, 16, 60, 2).cuda()
+    n, pos = torch.tensor(lengths, dtype=torch.int32).cuda(), torch.tensor(lengths).cuda() - 1
+    slots = table.long().gather(1, (pos // 16)[:, None])[:, 0] * 16 + pos % 16
+    x, r = (rand((B, K), torch.bfloat16, i).cuda() for i in (7, 8))
+    args = (slots, table, n, pos, frequencies(D // 2).cuda(), D)
+    one, two = Int8KVCache(*(t.clone() for t in cache)), Int8KVCache(*(t.clone() for t in cache))
+    y, h = step(w, x, r if res else None, one, *args, window=200)
+    y2, h2 = parts(w, x, r if res else None, two, *args, window=200)
+    assert torch.equal(y, y2) and torch.equal(h, h2) and all(torch.equal(a, b) for a, b in zip(one, two))
+    # leading dimensions, and several axes of positions
+    again = Int8KVCache(*(t.clone() for t in cache))
+    y3, h3 = step(w, x.view(5, 1, K), r.view(5, 1, K) if res else None, again, slots.view(5, 1), table, n,
+                  torch.stack([pos, pos]).view(2, 5, 1), *args[4:], window=200, sections=(D // 4, D // 2 - D // 4))
+    assert y3.shape == (5, 1, K) and torch.equal(y3.view(5, K), y) and torch.equal(h3.view(5, K), h)
+
+
+def test_decoding_in_a_graph():
+    """A prompt into the cache, then tokens one by one by a captured step whose lengths, positions and
+    slots move on the GPU; the attention of the last step against 64 bits."""
+    from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_append, int8_kv_cache
+    H, KV, D, K, B, page = 4, 2, 64, 256, 3, 16
+    w, freq = block(K, H, KV, D, 3), frequencies(D // 2).cuda()
+    prompts = [100, 1, 31]
+    order = torch.randperm(40, generator=torch.Generator().manual_seed(1)).int()
+    table = order[:36].view(3, 12).contiguous().cuda()
+
+    def fresh():
+        cache = int8_kv_cache(40, KV, D, page)
+        for b, m in enumerate(prompts):
+            qkv = rand((m, H + 2 * KV, D), torch.bfloat16, 20 + b).cuda()
+            t = torch.arange(m).cuda()
+            slots = table[b].long()[t // page] * page + t % page
+            int8_kv_append(*qkv.split([H, KV, KV], 1), cache, slots, t, freq, w["qw"], w["kw"], 1e-6)
+        return cache, torch.tensor(prompts, dtype=torch.int32).cuda()
+
+    def advance(cache, n, x):
+        n.add_(1)
+        pos = n.long() - 1
+        slots = table.long().gather(1, (pos // page)[:, None])[:, 0] * page + pos % page
+        return step(w, x, None, cache, slots, table, n, pos, freq, D)[0]
+    xs = [rand((B, K), torch.bfloat16, 30 + i).cuda() for i in range(20)]
+    cache, n = fresh()
+    want = [advance(cache, n, x) for x in xs]
+    end = [t.clone() for t in cache]
+
+    cache, n = fresh()
+    x = xs[0].clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        advance(cache, n, x)
+    torch.cuda.current_stream().wait_stream(s)
+    n.sub_(1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = advance(cache, n, x)
+    for i in range(20):
+        x.copy_(xs[i])
+        graph.replay()
+        assert torch.equal(got, want[i]), i
+        torch.cuda.synchronize()
+        rand((4, 4), torch.bfloat16, i).cuda().sum()  # eager work in between
+    assert all(torch.equal(a, b) for a, b in zip(cache, end))
+    c = dict(q=rand((B, H, D), torch.bfloat16, 60), cache=[t.cpu() for t in cache], table=table.cpu(),
+             lengths=n.tolist(), dtype="bf16")
+    assert c["lengths"] == [m + 20 for m in prompts]
+    check(c)
+
+
+def test_two_graphs_share_memory():
+    """Workspaces of two captured graphs in one pool, replayed in turn."""
+    c, d = case([5000, 700], 4, 2, 64, 16, "bf16", 18), case([40, 6000], 4, 2, 64, 16, "bf16", 19)
+    from mxfp4_quantized_gemm_amd.attention import paged_attention
+    args = [(x["q"].cuda(), [t.cuda() for t in x["cache"]], x["table"].cuda(),
+             torch.tensor(x["lengths"], dtype=torch.int32).cuda()) for x in (c, d)]
+    want = [paged_attention(*a) for a in args]
+    torch.cuda.synchronize()
+    graphs, outs, pool = [], [], None
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            outs.append(paged_attention(*a))
+        pool = g.pool()
+        graphs.append(g)
+    for i in range(6):
+        graphs[i % 2].replay()
+        got = outs[i % 2].clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want[i % 2]), i
