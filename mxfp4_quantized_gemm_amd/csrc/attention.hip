@@ -8,29 +8,43 @@
 // keeps the running maximum, sum and output of its tokens, and they are joined
 // at the end.
 //
-// Work. A line is a key head of a sequence with up to 16 of its query heads; its
-// tokens are cut into units of 128, and the work-groups share the units of all
-// lines evenly, whatever the sequences' lengths: work-group w takes units [w U /
-// W, (w + 1) U / W) of all U, in order of sequence, line and token. A line that
+// Work. A line is a key head of a sequence with up to 16 of its query heads. A
+// work-group takes a line, or a part of it of the same number of tokens for all
+// lines (line_kernel; 256 parts in all keep the GPU busy). Where parts would be
+// longer than 4096 tokens, and one long sequence among short ones would be waited for,
+// lines are cut into units of 128 tokens and the work-groups share the units of all
+// lines evenly, whatever the sequences' lengths (attention_kernel): work-group w takes
+// units [w U / W, (w + 1) U / W) of all U, in order of sequence, line and token. A line that
 // one work-group has whole is written by it; of the others every work-group
-// leaves maximum, sum and output in the workspace (at most two lines a
-// work-group, its first and its last), and a second kernel joins them. The
+// leaves maximum, sum and output in the workspace, and a second kernel joins them. The
 // lengths stay on the GPU: a captured graph serves them as they grow.
+// (In a graph, 32 query and 8 key heads of 128, bf16: 16 x 1000 tokens 12.4 us in
+// parts, 15.9 shared evenly; 1 x 8000 10.6 and 15.9; 64 x 8000 167 and 170; 32 x 4000
+// 45.8 and 51.7.)
 //
 // A wave takes 32 tokens at a time, without LDS: the codes go from memory to
-// registers in the layout in which the matrix instructions (16x16x32, bf16,
-// fp32 sums) take them. Scores: rows are tokens, columns query heads; a lane
+// registers in the layout in which the matrix instructions (16x16x32, f16, fp32
+// sums) take them. Scores: rows are tokens, columns query heads; a lane
 // then has one head's scores of 4 tokens (twice), which is the layout that the
 // second product takes its probabilities in, if its k runs over the tokens in
 // the order (lane / 16) 4 + r of the first 16 and then of the last. Its rows
 // are the head's columns: a lane holds the values of 8 tokens in dim / 16
-// columns, so that bytes become bf16 pairs of two tokens without a move between
+// columns, so that bytes become f16 pairs of two tokens without a move between
 // lanes. Outputs have one head a lane, as the scores have.
 //
-// Precision. Codes are whole numbers below 2^7, exact in bf16. Queries enter as
-// the sum of one (bf16), two (fp16) or three (fp32) bf16 numbers, exact but for
-// fp32's values below 2^-110; p vs as the sum of two (error 2^-16 of each) for
-// 16-bit outputs, three (2^-24) for fp32. All sums are in fp32.
+// Codes to f16, two at a time: with the sign flipped a code c is the byte c + 128;
+// a permutation puts two of them into the low bytes of f16 words, where they are
+// the subnormals (c + 128) 2^-24, and a packed multiply-add with 2^15 and -2^-2
+// makes c 2^-9 of them, exact. (The conversion of a signed byte takes three times as
+// long as other instructions here: 7.0 against 2.2 to 2.5 ns a wave.)
+//
+// Precision. Queries are scaled by a power of two for each head, to a largest
+// value in [2^14, 2^15), and enter as one f16 number (bf16, fp16: exact but
+// for what lies 2^-39 below the largest) or as the sum of two (fp32: within 2^-24
+// of each, or 2^-39 of the largest). p vs is scaled by a power of two for the
+// largest vs so far, to below 2^14, and enters as one f16 number for bf16
+// outputs (2^-12 of each: an eighth of the output's own rounding), as the sum of
+// two for fp16 and fp32 (2^-24). All sums, the maximum and p are in fp32.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -41,7 +55,7 @@
 namespace mx {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = kUnitWaves, kThreads = 64 * kWaves;
@@ -63,6 +77,7 @@ struct Args {
   int batch, dim, kv, tiles, group;  // group: query heads a key head; tiles: lines a key head
   int page, most;                    // tokens of a page, and of a table's row
   int window;                        // 0: none
+  int splits, chunk;                 // line_kernel's parts of a line, and their tokens
   int rows;                          // heads of a line at most: min(group, 16)
   Divisor page16;                    // by page / 16
   float scale;                       // times log2(e)
@@ -71,11 +86,44 @@ struct Args {
 // A value that is the same in all lanes, for the compiler to know.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// prefix[b] = units a line of the sequences before b, for b <= batch.
-__device__ __forceinline__ void prefix_units(const Args& A, int64_t* prefix) {
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ int scan_lanes(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // within 16 lanes: shifted by 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 to the next 16, of each 32
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to the upper 32
+  return v;
+}
+
+// Units a line of the sequences before each: up to 64 sequences in the lanes of
+// every wave (their units sum to below 2^31), without a barrier, more in LDS.
+struct Plan {
+  int64_t* all;  // LDS: [batch + 1], or NULL
+  int length;    // this lane's sequence's,
+  int upto;      // its units and those before it
+  int64_t total;
+  __device__ __forceinline__ int length_of(const Args& A, int b) const {
+    return all != nullptr ? uniform(A.lengths[b]) : __builtin_amdgcn_readlane(length, b);
+  }
+  __device__ __forceinline__ int64_t before(int b) const {
+    if (all != nullptr) return all[b];
+    const int v = __builtin_amdgcn_readlane(upto, uniform(b > 0 ? b - 1 : 0));
+    return b > 0 ? v : 0;
+  }
+};
+__device__ __forceinline__ Plan plan_of(const Args& A, int64_t* prefix) {
   __shared__ int64_t sums[kWaves];
   constexpr int PER = kBatch / kThreads;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  Plan p{nullptr, 0, 0, 0};
+  if (A.batch <= 64) {
+    p.length = lane < A.batch ? A.lengths[lane] : 0;
+    p.upto = scan_lanes(span_of(p.length, A.most, A.window).units);
+    p.total = __builtin_amdgcn_readlane(p.upto, 63);
+    return p;
+  }
   int64_t own[PER], s = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -101,22 +149,32 @@ __device__ __forceinline__ void prefix_units(const Args& A, int64_t* prefix) {
   }
   if (threadIdx.x == 0) prefix[0] = 0;
   __syncthreads();
+  p.all = prefix;
+  p.total = prefix[A.batch];
+  return p;
 }
 
 // Codes and scales of 32 tokens, as a lane holds them.
 template <int DP>
 struct Raw {
-  uint32_t k[2][DP / 16];  // token lane % 16 (+ 16): bytes [lane / 16 * DP / 4, + DP / 4)
+  u32x4 k[2][DP / 64];     // the first (last) 16 tokens' codes: 16 bytes a lane, 1 KiB a load
   uint32_t v[8][DP / 64];  // token (lane / 16) 4 + j (+ 16): bytes [lane % 16 * DP / 16, + DP / 16)
-  f32x4 ks[2], vs[2];      // tokens (lane / 16) 4 + r (+ 16)
+  float scale;             // of token lane % 32: ks in lanes below 32, vs in the others
+  bool ok[2];              // whether the 16 tokens' page is in the cache
 };
+
+// The cache is read once: past the caches (64 x 8000 tokens: 169 us; 189 through them).
+template <class X>
+__device__ __forceinline__ X load_once(const void* p) {
+  return __builtin_nontemporal_load(static_cast<const X*>(p));
+}
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&d)[N]) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const u32x4 q = *reinterpret_cast<const u32x4*>(p + 4 * i);
+      const u32x4 q = load_once<u32x4>(p + 4 * i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[i + e] = q[e];
     }
@@ -127,81 +185,92 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&d)[N]) {
 #pragma unroll
     for (int e = 0; e < 3; ++e) d[e] = q[e];
   } else if constexpr (N == 2) {
-    const u32x2 q = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 q = load_once<u32x2>(p);
     d[0] = q.x;
     d[1] = q.y;
   } else {
-    d[0] = *reinterpret_cast<const uint32_t*>(p);
+    d[0] = load_once<uint32_t>(p);
   }
 }
 
-// Whether tokens [t, t + 16) lie in a page of the cache, and its row (uniform).
-struct Place {
-  bool ok;
-  int64_t row;  // of token t, in rows of all heads
+// Where a wave's next 32 tiles lie: lane 2 i + h has the page (as the table has
+// it) and the row in it of the 16 tokens from t + i step + 16 h on. Looked up
+// for 32 tiles at once, so that no tile's loads wait for a page's number.
+struct Places {
+  int id, off;
 };
-__device__ __forceinline__ Place place(const Args& A, const int32_t* table, int head, int t, int n) {
-  const int col = (int)divided((uint32_t)t >> 4, A.page16), off = t - col * A.page;
-  int id = t < n ? uniform(table[col]) : -1;
-  Place p;
-  p.ok = id >= 0 && id < A.cache_pages;
-  id = p.ok ? id : 0;
-  p.row = ((int64_t)id * A.kv + head) * A.page + off;
+__device__ __forceinline__ Places places(const Args& A, const int32_t* table, uint32_t t, int step, int lane) {
+  const uint32_t at = t + (uint32_t)(lane >> 1) * step + (lane & 1) * 16;  // may be past 2^31
+  const uint32_t col = divided(at >> 4, A.page16);                         // read where it is below
+  Places p;
+  p.off = (int)(at - col * A.page);
+  p.id = -1;
+  if (at < (uint32_t)A.most) p.id = table[col];
   return p;
 }
 
-template <int DP>
-__device__ __forceinline__ void load_tile(const Args& A, const Place& a, const Place& b, int lane,
-                                          Raw<DP>& r) {
-  const int c = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t row = h ? b.row : a.row;
-    load_words<DP / 16>(A.kc + row * DP + (c * DP + g * (DP / 4)), r.k[h]);
-    const uint8_t* v = A.vc + row * DP + (g * 4 * DP + c * (DP / 16));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) load_words<DP / 64>(v + j * DP, r.v[4 * h + j]);
-    r.ks[h] = *reinterpret_cast<const f32x4*>(A.ks + row + g * 4);
-    r.vs[h] = *reinterpret_cast<const f32x4*>(A.vs + row + g * 4);
-  }
+// The same as rows of the cache (of all heads), with a bit of `ok` for each 16
+// tokens whose page is in it; those of the others are in page 0.
+struct Rows16 {
+  int64_t row;
+  uint64_t ok;
+};
+__device__ __forceinline__ Rows16 rows_of_pages(const Args& A, Places p, int head) {
+  const bool ok = p.id >= 0 && p.id < A.cache_pages;
+  return {((int64_t)(ok ? p.id : 0) * A.kv + head) * A.page + p.off, __ballot(ok)};
+}
+__device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-__device__ __forceinline__ float byte_of(uint32_t q, int b) { return (float)(int8_t)(q >> (8 * b)); }
-// The upper halves of two floats, a in the low half: bf16 by truncation.
-__device__ __forceinline__ uint32_t upper(float a, float b) {
-  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+template <int DP>
+__device__ __forceinline__ void load_tile(const Args& A, const Rows16& p, int tile, int lane, Raw<DP>& r) {
+  const int c = lane & 15, g = lane >> 4;
+  int64_t row[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    row[h] = lane_of(p.row, 2 * tile + h);
+    r.ok[h] = p.ok >> (2 * tile + h) & 1;
+#pragma unroll
+    for (int i = 0; i < DP / 64; ++i) r.k[h][i] = load_once<u32x4>(A.kc + row[h] * DP + (1024 * i + 16 * lane));
+    const uint8_t* v = A.vc + row[h] * DP + (g * 4 * DP + c * (DP / 16));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_words<DP / 64>(v + j * DP, r.v[4 * h + j]);
+  }
+  r.scale = load_once<float>((lane & 32 ? A.vs : A.ks) + (lane & 16 ? row[1] : row[0]) + c);
+  __builtin_amdgcn_sched_barrier(0);  // all loads before what waits for the last tile's
 }
-__device__ __forceinline__ float truncated(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+
+constexpr uint32_t kFlip = 0x80808080u;  // codes to bytes code + 128
+// c 2^-9 of byte b of p and byte e of q (of flipped words), as an f16 pair.
+__device__ __forceinline__ uint32_t pair_of(uint32_t p, int b, uint32_t q, int e) {
+  const f16x2 up = {(_Float16)0x1p15f, (_Float16)0x1p15f}, off = {(_Float16)-0.25f, (_Float16)-0.25f};
+  const uint32_t u = __builtin_amdgcn_perm(q, p, 0x0c000c00u | (uint32_t)(4 + e) << 16 | (uint32_t)b);
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2, u), up, off));
+}
 
 struct Frag {
   uint32_t w[4];
-  __device__ __forceinline__ bf16x8 v() const {
+  __device__ __forceinline__ f16x8 v() const {
     const u32x4 q = {w[0], w[1], w[2], w[3]};
-    return __builtin_bit_cast(bf16x8, q);
+    return __builtin_bit_cast(f16x8, q);
   }
 };
+__device__ __forceinline__ f32x4 mfma(const Frag& a, const Frag& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v(), b.v(), c, 0, 0, 0);
+}
 
-// v as the sum of N bf16 numbers, each the rest's upper 8 bits (the last one
-// rounded); not finite: the first one alone.
+// v as the sum of N f16 numbers, each the rest rounded to nearest.
 template <int N>
 __device__ __forceinline__ void split(const float (&v)[8], Frag (&f)[N]) {
-  float r[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = v[j];
-#pragma unroll
-  for (int p = 0; p < N; ++p) {
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      if (p + 1 < N || N == 1) {
-        f[p].w[j / 2] = upper(r[j], r[j + 1]);
-      } else {
-        const bf16x2 h = {(__bf16)r[j], (__bf16)r[j + 1]};
-        f[p].w[j / 2] = __builtin_bit_cast(uint32_t, h);
-      }
-    }
-    if (p + 1 < N) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] -= truncated(r[j]);
+  for (int j = 0; j < 8; j += 2) {
+    const f16x2 h = {(_Float16)v[j], (_Float16)v[j + 1]};
+    f[0].w[j / 2] = __builtin_bit_cast(uint32_t, h);
+    if constexpr (N > 1) {
+      const f16x2 r = {(_Float16)(v[j] - (float)h.x), (_Float16)(v[j + 1] - (float)h.y)};
+      f[1].w[j / 2] = __builtin_bit_cast(uint32_t, r);
     }
   }
 }
@@ -211,118 +280,260 @@ __device__ __forceinline__ float max_groups(float v) {
   return far_lane<X>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
+// K's codes pass through LDS, a wave's tile through 2 to 9 KiB of its own: the
+// matrix instruction's lanes hold 16 tokens side by side, whose rows, loaded so,
+// are 16 cache lines for every 16 lanes (64 x 8000 tokens: 174 us); loaded row after
+// row a 16th of that (169). Rows have 16 bytes more there, so that 16 tokens' reads
+// meet in no bank.
+template <int DP>
+constexpr int kPitch = DP + 16;
+
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// A work-group's LDS: what its waves stage, then their sums.
+template <int DP, int NW>
+union Shared {
+  uint8_t stage[NW][kTile * kPitch<DP> + 256];
+  float all[NW][kGroup][DP + 4];
+};
+
+constexpr float kSmallest = 0x1p-112f;  // so that 2^14 over it is in fp32's range
+
 template <int T, int DP, int QP, int PP>
 struct Wave {
   static constexpr int KS = DP / 32, NB = DP / 16;
   Frag q[KS][QP];
-  f32x4 acc[NB];
-  float m, l;
+  f32x4 acc[NB];  // sum of p vs c, times 2^14 / top_vs and 2^-9
+  float hs;       // scores are sums of codes times this and ks
+  float m, l;     // scores' maximum, sum of p (of this lane's tokens)
+  float top_vs;   // a power of two above the scales so far,
+  float unit;     // 2^14 over it
+  uint8_t* stage; // this wave's LDS: 32 rows of K's codes, their ks and vs
 
-  __device__ __forceinline__ void start(const Args& A, int b, int head0, int heads, int lane) {
-    const int c = lane & 15, g = lane >> 4;
-    const int64_t at = b * A.q.ts + (head0 + min(c, heads - 1)) * A.q.hs;
+  // The first of 8 columns that lanes of group g have in k-step s of the scores.
+  static __device__ __forceinline__ int column(int s, int g) { return (g + 4 * (s / 2)) * 16 + 8 * (s & 1); }
+
+  // The queries of a lane's head (of the last one in the lanes past it, whose
+  // results nobody reads), loaded early and converted when the first codes are
+  // on their way.
+  static constexpr int V = 16 / Type<T>::S;  // values of a load
+  __device__ __forceinline__ void load_queries(const Args& A, int b, int head0, int heads, int lane,
+                                               float (&v)[KS][8]) {
+    const int64_t at = b * A.q.ts + (head0 + min(lane & 15, heads - 1)) * A.q.hs;
+    if (A.dim % 8 == 0) {
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      float v[8];
-      const int d = g * (DP / 4) + 8 * s;
-      constexpr int S = Type<T>::S, V = 16 / S;
-      if (A.dim % 8 == 0) {
+      for (int s = 0; s < KS; ++s) {
+        // columns past the head: the first ones' values, replaced below
+        const int d = column(s, lane >> 4), from = d < A.dim ? d : 0;
 #pragma unroll
         for (int k = 0; k < 8; k += V) {
-          float e[V] = {};
-          if (c < heads && d < A.dim)
-            unpack<T, V>(*reinterpret_cast<const u32x4_2*>(static_cast<const uint8_t*>(A.q.p) + (at + d + k) * S), e);
+          float e[V];
+          unpack<T, V>(*reinterpret_cast<const u32x4_2*>(static_cast<const uint8_t*>(A.q.p) + (at + from + k) * Type<T>::S), e);
 #pragma unroll
-          for (int j = 0; j < V; ++j) v[k + j] = e[j];
+          for (int j = 0; j < V; ++j) v[s][k + j] = e[j];
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c < heads && d + j < A.dim ? get1<T>(A.q.p, at + d + j) : 0.f;
       }
-      split<QP>(v, q[s]);
+    } else {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[s][j] = get1<T>(A.q.p, at + min(column(s, lane >> 4) + j, A.dim - 1));
+    }
+  }
+
+  __device__ __forceinline__ void start(const Args& A, float (&v)[KS][8], int lane) {
+    if (A.dim < DP) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[s][j] = column(s, lane >> 4) + j < A.dim ? v[s][j] : 0.f;
+    }
+    float big = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(v[s][j]));  // (a NaN is passed over)
+    if (__any(big == __builtin_inff())) {
+      big = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(v[s][j]) < __builtin_inff() ? fabsf(v[s][j]) : 0.f);
+    }
+    big = max_groups<32>(max_groups<16>(big));
+    const int up = big > 0.f ? 15 - __builtin_amdgcn_frexp_expf(big) : 0;  // big 2^up in [2^14, 2^15)
+    hs = __builtin_amdgcn_ldexpf(A.scale, 9 - up);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[s][j] = __builtin_amdgcn_ldexpf(v[s][j], up);
+      split<QP>(v[s], q[s]);
       if constexpr (QP > 1) {
-        // the rest of an infinity is no number: it stands alone, and so does a NaN,
-        // whose upper half might be an infinity's
+        // the rest of an infinity is no number: it stands alone
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (!__builtin_isfinite(v[j])) {
-            if (v[j] != v[j]) q[s][0].w[j / 2] |= j & 1 ? 0x400000u : 0x40u;
-#pragma unroll
-            for (int p = 1; p < QP; ++p) q[s][p].w[j / 2] &= j & 1 ? 0xffffu : 0xffff0000u;
-          }
+          if (!__builtin_isfinite(v[s][j])) q[s][1].w[j / 2] &= j & 1 ? 0xffffu : 0xffff0000u;
       }
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     m = kNone;
     l = 0.f;
+    top_vs = kSmallest;
+    unit = 0x1p14f / kSmallest;
   }
 
-  // 32 tokens from t on; `whole`: all of them count.
-  __device__ __forceinline__ void tile(const Args& A, const Raw<DP>& r, bool whole, bool oka, bool okb,
-                                       int t, const Span& sp, int lane) {
+  // 32 tokens from t on.
+  __device__ __forceinline__ void tile(const Args& A, const Raw<DP>& r, int t, const Span& sp, int lane) {
     const int g = lane >> 4;
-    float s[8], vs[8];
+    f32x4 sc[2] = {};
+    wave_sync();  // the last tile's reads are done
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i) {
+        const int at = 64 * i + lane;
+        *reinterpret_cast<u32x4*>(stage + (16 * h + at / (DP / 16)) * kPitch<DP> + at % (DP / 16) * 16) = r.k[h][i] ^ kFlip;
+      }
+    float* const scales = reinterpret_cast<float*>(stage + kTile * kPitch<DP>);
+    scales[lane] = r.scale;
+    wave_sync();
+    f32x4 kss[2], vss[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+      kss[h] = *reinterpret_cast<const f32x4*>(scales + 16 * h + 4 * g);
+      vss[h] = *reinterpret_cast<const f32x4*>(scales + 32 + 16 * h + 4 * g);
+    }
+    u32x4 codes[2][DP / 64];
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        Frag f;
+    for (int i = 0; i < DP / 64; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        codes[h][i] = *reinterpret_cast<const u32x4*>(stage + (16 * h + (lane & 15)) * kPitch<DP> + (g + 4 * i) * 16);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      Frag f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t w = r.k[h][2 * k + j / 2];
-          f.w[j] = upper(byte_of(w, 2 * (j & 1)), byte_of(w, 2 * (j & 1) + 1));
+          const uint32_t w = codes[h][k / 2][2 * (k & 1) + j / 2];
+          f[h].w[j] = pair_of(w, 2 * (j & 1), w, 2 * (j & 1) + 1);
         }
 #pragma unroll
-        for (int p = 0; p < QP; ++p)
-          sc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.v(), q[k][p].v(), sc, 0, 0, 0);
-      }
+      for (int p = 0; p < QP; ++p)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[4 * h + e] = sc[e] * (r.ks[h][e] * A.scale);
-        vs[4 * h + e] = r.vs[h][e];
-      }
+        for (int h = 0; h < 2; ++h) sc[h] = mfma(f[h], q[k][p], sc[h]);
     }
-    if (!whole) {
+    float s[8], vs[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s[e] = sc[e / 4][e & 3] * (kss[e / 4][e & 3] * hs);
+      vs[e] = vss[e / 4][e & 3];
+    }
+    if (!(r.ok[0] && r.ok[1] && t >= sp.first && t + kTile <= sp.n)) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int at = t + (e & 4) * 4 + g * 4 + (e & 3);
-        const bool in = (e & 4 ? okb : oka) && at >= sp.first && at < sp.n;
+        const bool in = r.ok[e / 4] && at >= sp.first && at < sp.n;
         s[e] = in ? s[e] : kNone;
         vs[e] = in ? vs[e] : 0.f;
       }
     }
-    float top = s[0];
+    float top = s[0], big = fabsf(vs[0]);
 #pragma unroll
-    for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
-    if (__any(top > m)) {  // rare after the first tiles
+    for (int e = 1; e < 8; ++e) {
+      top = fmaxf(top, s[e]);
+      big = fmaxf(big, fabsf(vs[e]));
+    }
+    if (__any(top > m || big >= top_vs)) {  // rare after the first tiles
       const float now = fmaxf(m, max_groups<32>(max_groups<16>(top)));
+      big = max_groups<32>(max_groups<16>(big));
+      // the power of two above (2^127 at most: a scale past it is as good as infinite)
+      const float above = __uint_as_float(min((__float_as_uint(big) & 0x7f800000u) + 0x800000u, 0x7f000000u));
+      const float vs_now = fmaxf(top_vs, above);
       const float a = now == m ? 1.f : __builtin_amdgcn_exp2f(m - now);
+      const float o = a * (top_vs / vs_now);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) acc[i] *= a;
+      for (int i = 0; i < NB; ++i) acc[i] *= o;
       l *= a;
       m = now;
+      top_vs = vs_now;
+      unit = 0x1p14f / vs_now;
     }
     const float ref = m == kNone ? 0.f : m;
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float p = __builtin_amdgcn_exp2f(s[e] - ref);
-      l += p;
-      w[e] = p * vs[e];
+      w[e] = p * (vs[e] * unit);
+      s[e] = p;
     }
+    l += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     Frag pf[PP];
     split<PP>(w, pf);
+    uint32_t v[8][DP / 64];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      Frag f;
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        f.w[j] = upper(byte_of(r.v[2 * j][i / 4], i & 3), byte_of(r.v[2 * j + 1][i / 4], i & 3));
+      for (int i = 0; i < DP / 64; ++i) v[j][i] = r.v[j][i] ^ kFlip;
+#pragma unroll
+    for (int i = 0; i < NB; i += 2) {
+      Frag f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          f[h].w[j] = pair_of(v[2 * j][i / 4], (i + h) & 3, v[2 * j + 1][i / 4], (i + h) & 3);
 #pragma unroll
       for (int p = 0; p < PP; ++p)
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.v(), pf[p].v(), acc[i], 0, 0, 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) acc[i + h] = mfma(f[h], pf[p], acc[i + h]);
+    }
+  }
+
+  // Tiles at t, t + step, ... below `end`; p: where the first ones lie; v: the
+  // queries. With AHEAD > 0 that many tiles' loads are on their way during one's
+  // products. They are made in any case then (behind the last tile: the last one's again),
+  // because what waits for a tile's loads counts those behind them: with loads under a
+  // condition it waited for the next tile's too.
+  template <int AHEAD>
+  __device__ __forceinline__ void run(const Args& A, const int32_t* table, Places p, int head, int t, int step,
+                                      int end, const Span& sp, float (&v)[KS][8], int lane) {
+    constexpr int BUFS = AHEAD + 1, BATCH = 32 / BUFS * BUFS;
+    Raw<DP> r[BUFS];
+    int left = t < end ? uniform((int)((uint32_t)(end - t + step - 1) / (uint32_t)step)) : 0;  // from the batch's first on
+    Places then = p;
+    Rows16 now = rows_of_pages(A, p, head);
+#pragma unroll
+    for (int j = 0; j < (AHEAD > 0 ? AHEAD : 1); ++j) load_tile<DP>(A, now, max(min(j, left - 1), 0), lane, r[j]);
+    start(A, v, lane);
+    if (left == 0) return;
+    for (int i = 0;;) {
+      if (i == 0) then = places(A, table, (uint32_t)t + (uint32_t)(BATCH * step), step, lane);
+      const Rows16 next = i + BUFS == BATCH ? rows_of_pages(A, then, head) : now;  // needed from here on
+#pragma unroll
+      for (int j = 0; j < BUFS; ++j) {
+        const int k = min(i + j + (AHEAD > 0 ? AHEAD : 1), left - 1);
+        const auto ahead = [&]() {
+          load_tile<DP>(A, k < BATCH ? now : next, k < BATCH ? k : k - BATCH, lane, r[(j + AHEAD) % BUFS]);
+        };
+        if (AHEAD > 0) ahead();
+        tile(A, r[j], t, sp, lane);
+        t += step;
+        if (t >= end) return;
+        if (AHEAD == 0) ahead();
+      }
+      i += BUFS;
+      if (i == BATCH) {
+        i = 0;
+        left -= BATCH;
+        now = next;
+      }
     }
   }
 };
@@ -335,18 +546,68 @@ __device__ __forceinline__ void finish(const Args& A, int64_t row, int d, float 
   if (d == 0 && A.lse != nullptr) A.lse[row] = l == 0.f ? kNone : (m + __log2f(l)) * 0.69314718f;
 }
 
+// The waves' sums of a line meet in LDS: its output, or (part not NULL) the sums
+// for another kernel to join. `u` is in a wave's registers until here.
+template <int T, int DP, int NW, class W>
+__device__ __forceinline__ void meet(const Args& A, Shared<DP, NW>& lds, const W& u, int wave, int lane, int b, int head0, int heads,
+                                     float* part) {
+  auto& all = lds.all;
+  __syncthreads();  // the waves are done with what they staged
+  __shared__ float all_m[NW][kGroup], all_l[NW][kGroup];
+  const int hh = lane & 15, g = lane >> 4, thread = wave * 64 + lane;
+  float l = u.l;
+  l = far_lane<16>(l, add32);
+  l = far_lane<32>(l, add32);
+  const float unit = u.top_vs * 0x1p-5f;  // of acc: 2^9 top_vs / 2^14
+  if (hh < heads) {
+#pragma unroll
+    for (int i = 0; i < DP / 16; i += 4)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<f32x4*>(&all[wave][hh][(g * 4 + r) * (DP / 16) + i]) =
+            f32x4{u.acc[i][r], u.acc[i + 1][r], u.acc[i + 2][r], u.acc[i + 3][r]} * unit;
+    if (g == 0) {
+      all_m[wave][hh] = u.m;
+      all_l[wave][hh] = l;
+    }
+  }
+  __syncthreads();
+  for (int i = thread; i < heads * DP; i += 64 * NW) {
+    const int h = i / DP, d = i % DP;
+    float M = all_m[0][h];
+#pragma unroll
+    for (int k = 1; k < NW; ++k) M = fmaxf(M, all_m[k][h]);
+    float L = 0.f, v = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float f = all_m[k][h] == M ? 1.f : __builtin_amdgcn_exp2f(all_m[k][h] - M);
+      L = fmaf(f, all_l[k][h], L);
+      v = fmaf(f, all[k][h][d], v);
+    }
+    if (part == nullptr) {
+      if (d < A.dim) finish<T>(A, (int64_t)b * A.q.heads + head0 + h, d, v, M, L);
+    } else {
+      part[h * (DP + 2) + d] = v;
+      if (d == 0) part[h * (DP + 2) + DP] = M;
+      if (d == 0) part[h * (DP + 2) + DP + 1] = L;
+    }
+  }
+  __syncthreads();
+}
+
+// Lines shared evenly by the work-groups.
 template <int T, int DP, int QP, int PP>
 __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(Args A) {
   __shared__ int64_t prefix[kBatch + 1];
-  __shared__ float all[kWaves][kGroup][DP + 4];
-  __shared__ float all_m[kWaves][kGroup], all_l[kWaves][kGroup];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  prefix_units(A, prefix);
+  __shared__ Shared<DP, kWaves> lds;
+  const int wave = threadIdx.x >> 6;
+  int lane = threadIdx.x & 63;
+  const Plan plan = plan_of(A, prefix);
   const int lines = A.kv * A.tiles;
-  const int64_t U = prefix[A.batch] * lines;
+  const int64_t U = plan.total * lines;
   // sequences without a token
   for (int b = blockIdx.x; b < A.batch; b += gridDim.x)
-    if (prefix[b + 1] == prefix[b])
+    if (plan.before(b + 1) == plan.before(b))
       for (int i = threadIdx.x; i < (int)A.q.heads * A.dim; i += kThreads)
         finish<T>(A, (int64_t)b * A.q.heads + i / A.dim, i % A.dim, 0.f, 0.f, 0.f);
   if (U == 0) return;
@@ -354,116 +615,115 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
   if (w >= W) return;
   const int64_t lo = share(w, U, W), hi = share(w + 1, U, W);
   int b = 0;  // the last sequence that starts at or before lo and has a unit
-  for (int at = A.batch, from = 0; from < at;) {
-    const int mid = (from + at) / 2;
-    if (prefix[mid + 1] * lines > lo) {
-      at = mid;
-    } else {
-      from = mid + 1;
+  if (plan.all == nullptr) {
+    b = __popcll(__ballot(lane < A.batch && (int64_t)plan.upto * lines <= lo));
+  } else {
+    for (int at = A.batch, from = 0; from < at;) {
+      const int mid = (from + at) / 2;
+      if (prefix[mid + 1] * lines > lo) {
+        at = mid;
+      } else {
+        from = mid + 1;
+      }
+      b = at;
     }
-    b = at;
   }
   for (int64_t u = lo; u < hi;) {
-    while (prefix[b + 1] * lines <= u) ++b;
+    asm volatile("" : "+v"(lane));  // else what a line needs of it is kept over all lines, and spills
+    while (plan.before(b + 1) * lines <= u) ++b;
     b = uniform(b);
-    const Span sp = span_of(uniform(A.lengths[b]), A.most, A.window);
-    const int64_t in = u - prefix[b] * lines;
-    const int line = uniform((int)(in / sp.units)), unit = uniform((int)(in - (int64_t)line * sp.units));
+    const Span sp = span_of(plan.length_of(A, b), A.most, A.window);
+    const int64_t in = u - plan.before(b) * lines;
+    const int line = uniform((int)quotient(in, sp.units)), unit = uniform((int)(in - (int64_t)line * sp.units));
     const int count = uniform((int)min(hi - u, (int64_t)(sp.units - unit)));
     const int head = line / A.tiles, tile = line - head * A.tiles;
     const int head0 = head * A.group + tile * kGroup, heads = min(A.group - tile * kGroup, kGroup);
     const int32_t* table = A.table + b * A.table_ld;
-    Wave<T, DP, QP, PP> W_;
-    W_.start(A, b, head0, heads, lane);
-    int t = uniform(sp.start + unit * kUnit + wave * kTile);
-    const int end = min(sp.n, sp.start + (unit + count) * kUnit);
-    Raw<DP> next;
-    Place a{false, 0}, c{false, 0};
-    if (t < end) {
-      a = place(A, table, head, t, sp.n);
-      c = place(A, table, head, t + 16, sp.n);
-      load_tile<DP>(A, a, c, lane, next);
-    }
-    while (t < end) {
-      const Raw<DP> now = next;
-      const bool oka = a.ok, okc = c.ok;
-      const int tn = t + kUnit;
-      if (tn < end) {
-        a = place(A, table, head, tn, sp.n);
-        c = place(A, table, head, tn + 16, sp.n);
-        load_tile<DP>(A, a, c, lane, next);
-      }
-      W_.tile(A, now, oka && okc && t >= sp.first && t + kTile <= sp.n, oka, okc, t, sp, lane);
-      t = tn;
-    }
-    // the four waves' sums meet
-    float l = W_.l;
-    l = far_lane<16>(l, add32);
-    l = far_lane<32>(l, add32);
-    const int hh = lane & 15, g = lane >> 4;
-    if (hh < heads) {
-#pragma unroll
-      for (int i = 0; i < DP / 16; i += 4)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          *reinterpret_cast<f32x4*>(&all[wave][hh][(g * 4 + r) * (DP / 16) + i]) =
-              f32x4{W_.acc[i][r], W_.acc[i + 1][r], W_.acc[i + 2][r], W_.acc[i + 3][r]};
-      if (g == 0) {
-        all_m[wave][hh] = W_.m;
-        all_l[wave][hh] = l;
-      }
-    }
-    __syncthreads();
-    const bool complete = count == sp.units;
+    const int t = uniform(sp.start + unit * kUnit + wave * kTile);
+    const int end = uniform(min(sp.n, sp.start + (unit + count) * kUnit));
+    const Places p = places(A, table, t, kUnit, lane);
+    typedef Wave<T, DP, QP, PP> Sums;
+    Sums sums;
+    sums.stage = lds.stage[wave];
+    float q[Sums::KS][8];
+    sums.load_queries(A, b, head0, heads, lane, q);
+    sums.template run<1>(A, table, p, head, t, kUnit, end, sp, q, lane);
     // a work-group's first line has its first slot, its last line the second
-    float* part = A.ws + (2 * w + (u == lo ? 0 : 1)) * (int64_t)A.rows * (DP + 2);
-    for (int i = threadIdx.x; i < heads * DP; i += kThreads) {
-      const int h = i / DP, d = i % DP;
-      float M = all_m[0][h];
-#pragma unroll
-      for (int k = 1; k < kWaves; ++k) M = fmaxf(M, all_m[k][h]);
-      float L = 0.f, v = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) {
-        const float f = all_m[k][h] == M ? 1.f : __builtin_amdgcn_exp2f(all_m[k][h] - M);
-        L = fmaf(f, all_l[k][h], L);
-        v = fmaf(f, all[k][h][d], v);
-      }
-      if (complete) {
-        if (d < A.dim) finish<T>(A, (int64_t)b * A.q.heads + head0 + h, d, v, M, L);
-      } else {
-        part[h * (DP + 2) + d] = v;
-        if (d == 0) part[h * (DP + 2) + DP] = M;
-        if (d == 0) part[h * (DP + 2) + DP + 1] = L;
-      }
-    }
-    __syncthreads();
+    meet<T, DP, kWaves>(A, lds, sums, wave, lane, b, head0, heads,
+                        count == sp.units ? nullptr : A.ws + (2 * w + (u == lo ? 0 : 1)) * (int64_t)A.rows * (DP + 2));
     u += count;
   }
 }
 
-// Joins the lines that several work-groups have: one work-group a query head,
-// 8 parts at a time, each by 32 threads.
-template <int T, int DP>
-__global__ __launch_bounds__(kThreads) void join_kernel(Args A, int64_t groups) {
-  __shared__ int64_t prefix[kBatch + 1];
-  __shared__ float all[8][DP], all_m[8], all_l[8];
-  prefix_units(A, prefix);
-  const int b = blockIdx.x / (int)A.q.heads, head = blockIdx.x % (int)A.q.heads;
+// A work-group a line, or one of A.splits parts of it, each of A.chunk tokens.
+template <int T, int DP, int QP, int PP, int NW>
+__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : T == kF32 ? 2 : 4) void line_kernel(Args A) {
+  __shared__ Shared<DP, NW> lds;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int lines = A.kv * A.tiles;
-  const int64_t U = prefix[A.batch] * lines, units = prefix[b + 1] - prefix[b];
-  if (units == 0) return;
-  const int64_t W = min(groups, U);
-  const int tile = head % A.group / kGroup, row = head % A.group % kGroup;
-  const int64_t L0 = prefix[b] * lines + (head / A.group * A.tiles + tile) * units;
-  const int64_t first = owner(L0, U, W), last = owner(L0 + units - 1, U, W);
-  if (first == last) return;  // written already
+  const int part = blockIdx.x % A.splits, of = blockIdx.x / A.splits, b = of / lines, line = of - b * lines;
+  const int head = line / A.tiles, tile = line - head * A.tiles;
+  const int head0 = head * A.group + tile * kGroup, heads = min(A.group - tile * kGroup, kGroup);
+  const int32_t* table = A.table + b * A.table_ld;
+  const int length = A.lengths[b];
+  typedef Wave<T, DP, QP, PP> Sums;
+  Sums sums;
+  sums.stage = lds.stage[wave];
+  float q[Sums::KS][8];
+  sums.load_queries(A, b, head0, heads, lane, q);
+  Places p{-1, 0};
+  // without a window the pages are looked up before the length is there
+  const int from = part * A.chunk + wave * kTile;
+  if (A.window == 0) p = places(A, table, uniform(from), NW * kTile, lane);
+  const Span sp = span_of(uniform(length), A.most, A.window);
+  if (part > 0 && sp.start + part * A.chunk >= sp.n) return;
+  const int t = uniform(sp.start + from);
+  if (A.window != 0) p = places(A, table, t, NW * kTile, lane);
+  sums.template run<0>(A, table, p, head, t, NW * kTile, min(sp.n, sp.start + (part + 1) * A.chunk), sp, q,
+                       lane);
+  meet<T, DP, NW>(A, lds, sums, wave, lane, b, head0, heads,
+                  sp.n - sp.start <= A.chunk ? nullptr : A.ws + (int64_t)blockIdx.x * A.rows * (DP + 2));
+}
+
+// Joins the lines that several work-groups have: one work-group a query head, 8
+// parts at a time, each by 32 threads. CUT: as line_kernel cuts them, else as
+// attention_kernel does.
+template <int T, int DP, bool CUT>
+__global__ __launch_bounds__(kThreads) void join_kernel(Args A, int64_t groups) {
+  __shared__ int64_t prefix[CUT ? 1 : kBatch + 1];
+  __shared__ float all[8][DP], all_m[8], all_l[8];
+  const int b = blockIdx.x / (int)A.q.heads, head = blockIdx.x % (int)A.q.heads;
+  const int lines = A.kv * A.tiles, tile = head % A.group / kGroup, row = head % A.group % kGroup;
+  const int line = head / A.group * A.tiles + tile;
+  int64_t first, last, slot;  // parts; the slot of the first one
+  int step;                   // slots from part to part
+  if constexpr (CUT) {
+    const Span sp = span_of(A.lengths[b], A.most, A.window);
+    first = 0;
+    last = (sp.n - sp.start - 1) / A.chunk;
+    slot = ((int64_t)b * lines + line) * A.splits;
+    step = 1;
+  } else {
+    const Plan plan = plan_of(A, prefix);
+    const int64_t U = plan.total * lines, units = plan.before(b + 1) - plan.before(b);
+    if (units == 0) return;
+    const int64_t W = min(groups, U), L0 = plan.before(b) * lines + line * units;
+    first = owner(L0, U, W);
+    last = owner(L0 + units - 1, U, W);
+    slot = 2 * first;
+    step = 2;
+    // of the first one's two slots the line has the second if another line begins in it
+    if (share(first, U, W) < L0) slot |= int64_t(1) << 62;
+  }
+  if (first >= last) return;  // written already
+  const bool second = slot >> 62 & 1;
+  slot &= ~(int64_t(1) << 62);
   const int q = threadIdx.x >> 5, t = threadIdx.x & 31;
   constexpr int C = DP / 32;
   float v[C] = {}, m = kNone, l = 0.f;
   for (int64_t w = first + q; w <= last; w += 8) {
-    const int slot = w == first && share(w, U, W) < L0 ? 1 : 0;
-    const float* part = A.ws + ((2 * w + slot) * A.rows + row) * (int64_t)(DP + 2);
+    const int64_t at = slot + (w - first) * step + (w == first && second ? 1 : 0);
+    const float* part = A.ws + (at * A.rows + row) * (int64_t)(DP + 2);
     const float pm = part[DP], pl = part[DP + 1], now = fmaxf(m, pm);
     const float a = m == now ? 1.f : __builtin_amdgcn_exp2f(m - now);
     const float f = pm == now ? 1.f : __builtin_amdgcn_exp2f(pm - now);
@@ -497,30 +757,59 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args A, int64_t groups) 
 int pitch_of(int64_t dim) { return (int)((dim + 63) / 64 * 64); }
 int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
-// Work-groups of a launch: no more than there can be units.
-int64_t groups_of(int64_t batch, int64_t lines, int64_t most) {
-  return min64(kMaxGroups, batch * lines * ((most + kUnit - 1) / kUnit));
+// How a launch is cut. Lines in parts of at most kChunk tokens where that is
+// enough to keep the GPU busy, or the lines are many: a table's room is what the
+// host knows, and short sequences leave parts without work, but none waits
+// for a look at all lengths. Else the units shared evenly.
+struct Cut {
+  int64_t splits, chunk;  // splits 0: shared evenly
+  int64_t groups;
+};
+constexpr int64_t kCuts = 256, kChunk = 4096;
+// Tokens that line_kernel's waves take at a time.
+int64_t step_of(int64_t dim) { return pitch_of(dim) > 128 ? 4 * kTile : 8 * kTile; }
+// most: tokens that a line may have. Parts are cut for fewer than 512 lines, into
+// fewer than 512 more: below kMaxSlots, as many as twice the even shares.
+constexpr int64_t kMaxSlots = 2 * kMaxGroups;
+Cut cut_of(int64_t batch, int64_t lines, int64_t dim, int64_t most) {
+  const int64_t step = step_of(dim), steps = (most + step - 1) / step;
+  if (steps <= 1) return {1, step, batch * lines};
+  int64_t splits = min64(steps, (kCuts + batch * lines - 1) / (batch * lines));
+  const int64_t chunk = (steps + splits - 1) / splits * step;
+  splits = (most + chunk - 1) / chunk;
+  if (chunk <= kChunk) return {splits, chunk, batch * lines * splits};
+  return {0, 0, min64(kMaxGroups, batch * lines * ((most + kUnit - 1) / kUnit))};
 }
 
 template <int T, int DP, int QP, int PP>
-hipError_t go(const Args& A, int64_t groups, hipStream_t st) {
-  hipLaunchKernelGGL((attention_kernel<T, DP, QP, PP>), dim3((unsigned)(groups > 0 ? groups : 1)), dim3(kThreads),
-                     0, st, A);
-  hipError_t e = hipGetLastError();
-  // a line of one unit is never cut
-  if (e != hipSuccess || A.most <= kUnit) return e;
-  hipLaunchKernelGGL((join_kernel<T, DP>), dim3((unsigned)(A.batch * A.q.heads)), dim3(kThreads), 0, st, A,
-                     groups);
+hipError_t go(Args A, hipStream_t st) {
+  const Cut c = cut_of(A.batch, A.kv * A.tiles, A.dim, A.window > 0 ? min64(A.most, (int64_t)A.window + 15) : A.most);
+  const dim3 heads((unsigned)(A.batch * A.q.heads));
+  hipError_t e;
+  if (c.splits > 0) {
+    A.splits = (int)c.splits;
+    A.chunk = (int)c.chunk;
+    constexpr int NW = DP > 128 ? 4 : 8;
+    hipLaunchKernelGGL((line_kernel<T, DP, QP, PP, NW>), dim3((unsigned)c.groups), dim3(64 * NW), 0, st, A);
+    e = hipGetLastError();
+    if (e != hipSuccess || c.splits == 1) return e;
+    hipLaunchKernelGGL((join_kernel<T, DP, true>), heads, dim3(kThreads), 0, st, A, c.groups);
+  } else {
+    hipLaunchKernelGGL((attention_kernel<T, DP, QP, PP>), dim3((unsigned)c.groups), dim3(kThreads), 0, st, A);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((join_kernel<T, DP, false>), heads, dim3(kThreads), 0, st, A, c.groups);
+  }
   return hipGetLastError();
 }
 
 template <int T, int QP, int PP>
-hipError_t go_dim(const Args& A, int64_t groups, hipStream_t st) {
+hipError_t go_dim(const Args& A, hipStream_t st) {
   switch (pitch_of(A.dim)) {
-    case 64: return go<T, 64, QP, PP>(A, groups, st);
-    case 128: return go<T, 128, QP, PP>(A, groups, st);
-    case 192: return go<T, 192, QP, PP>(A, groups, st);
-    default: return go<T, 256, QP, PP>(A, groups, st);
+    case 64: return go<T, 64, QP, PP>(A, st);
+    case 128: return go<T, 128, QP, PP>(A, st);
+    case 192: return go<T, 192, QP, PP>(A, st);
+    default: return go<T, 256, QP, PP>(A, st);
   }
 }
 
@@ -528,10 +817,9 @@ hipError_t go_dim(const Args& A, int64_t groups, hipStream_t st) {
 
 size_t paged_attention_ws(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t table,
                           int64_t page_size) {
-  if (table * page_size <= kUnit) return 0;  // nothing to join
-  const int64_t group = q_heads / kv_heads, tiles = (group + kGroup - 1) / kGroup;
-  const int64_t groups = groups_of(min64(batch, kBatch), kv_heads * tiles, table * page_size);
-  return (size_t)groups * 2 * (size_t)min64(group, kGroup) * (size_t)(pitch_of(dim) + 2) * sizeof(float);
+  (void)batch;
+  if (table * page_size <= step_of(dim)) return 0;
+  return (size_t)kMaxSlots * (size_t)min64(q_heads / kv_heads, kGroup) * (size_t)(pitch_of(dim) + 2) * sizeof(float);
 }
 
 hipError_t launch_paged_attention(Heads q, int64_t batch, int64_t dim, int dtype, const mxfp4_int8_kv& cache,
@@ -564,10 +852,9 @@ hipError_t launch_paged_attention(Heads q, int64_t batch, int64_t dim, int dtype
     A.lse = lse ? lse + b * q.heads : nullptr;
     A.table = pages + b * pages_ld;
     A.lengths = lengths + b;
-    const int64_t groups = groups_of(A.batch, A.kv * A.tiles, A.most);
-    const hipError_t e = dtype == kBF16  ? go_dim<kBF16, 1, 2>(A, groups, stream)
-                         : dtype == kF16 ? go_dim<kF16, 2, 2>(A, groups, stream)
-                                         : go_dim<kF32, 3, 3>(A, groups, stream);
+    const hipError_t e = dtype == kBF16  ? go_dim<kBF16, 1, 1>(A, stream)
+                         : dtype == kF16 ? go_dim<kF16, 1, 2>(A, stream)
+                                         : go_dim<kF32, 2, 2>(A, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

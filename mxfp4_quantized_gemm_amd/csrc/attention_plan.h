@@ -30,11 +30,16 @@ MX_HD Span span_of(int length, int most, int window) {
   return s;
 }
 
+// a / b of numbers that are not negative: 64 bits take the GPU five times as long.
+MX_HD int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Of U units in a row, work-group w of W (W <= U) has [share(w), share(w + 1)).
-MX_HD int64_t share(int64_t w, int64_t U, int64_t W) { return w * U / W; }
+MX_HD int64_t share(int64_t w, int64_t U, int64_t W) { return quotient(w * U, W); }
 // The work-group that has unit u: the largest w with share(w) <= u, that is with w U
 // / W < u + 1.
-MX_HD int64_t owner(int64_t u, int64_t U, int64_t W) { return ((u + 1) * W - 1) / U; }
+MX_HD int64_t owner(int64_t u, int64_t U, int64_t W) { return quotient((u + 1) * W - 1, U); }
 
 // floor(x / d) = (x magic) >> shift for x < 2^27 and 1 <= d < 2^27: with d <= 2^s
 // and d magic = 2^(27 + s) + e, e < d, the excess x e / (d 2^(27 + s)) is below

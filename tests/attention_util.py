@@ -104,7 +104,9 @@ def attend64(q, cache, table, lengths, scale, window, dtype, parts_err):
     A score's error: the fp32 sum of dim products, ks * scale, its product with the sum and the
     difference to the maximum, (dim + 8) U of sum |q| |k| scale and 4 U of the score's size; with the exponential's two
     roundings that is e, relative to each probability. The sums over tokens add
-    (tokens + 64) U, the split of p vs parts_err, of sum p |v|."""
+    (tokens + 64) U, the split of p vs parts_err, of sum p |v|; and a p vs that is small is held to
+    2^-25 of an f16 subnormal's step where 2^14 stands for at most twice the largest vs: 2^-38 of
+    that for each code."""
     k, ks, v, vs = cache
     page, heads, dim = k.shape[2], k.shape[1], q.shape[2]
     out, lse, tol = [], [], []
@@ -130,6 +132,9 @@ def attend64(q, cache, table, lengths, scale, window, dtype, parts_err):
         mass = torch.einsum("hgn,nhd->hgd", p, vb.abs())
         err = torch.einsum("hgn,nhd->hgd", p * e, vb.abs()) + mass * (p * e).sum(-1, keepdim=True)
         err = err + mass * (parts_err + 2 * (len(t) + 64) * U)
+        codes = v[pg, :, t % page, :dim].double().abs().sum(0)  # [kv][dim]
+        top = vs[pg, :, t % page].double().abs().amax(0)
+        err = err + (2.0 ** -38 * top[:, None] * codes)[:, None]
         out.append(o.reshape(-1, dim))
         lse.append(torch.logsumexp(s, -1).reshape(-1))
         tol.append(err.reshape(-1, dim))

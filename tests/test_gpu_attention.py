@@ -7,7 +7,7 @@ import torch
 from tests.attention_util import TYPES, U, attend64, frequencies, half_step, make_cache, make_tables, near, rand
 
 pytestmark = pytest.mark.gpu
-PARTS = {"bf16": 2.0 ** -16, "fp16": 2.0 ** -16, "fp32": 3 * U}
+PARTS = {"bf16": 2.0 ** -12, "fp16": 2 * U, "fp32": 2 * U}
 
 
 def case(lengths, H, K, D, page, dtype, seed, size=2.0, spare=2):
