@@ -10,7 +10,7 @@
 //
 // Work. A line is a key head of a sequence with up to 16 of its query heads. A
 // work-group takes a line, or a part of it of the same number of tokens for all
-// lines (line_kernel; 256 parts in all keep the GPU busy). Where parts would be
+// lines (line_kernel). Where parts would be
 // longer than 4096 tokens, and one long sequence among short ones would be waited for,
 // lines are cut into units of 128 tokens and the work-groups share the units of all
 // lines evenly, whatever the sequences' lengths (attention_kernel): work-group w takes
@@ -18,9 +18,6 @@
 // one work-group has whole is written by it; of the others every work-group
 // leaves maximum, sum and output in the workspace, and a second kernel joins them. The
 // lengths stay on the GPU: a captured graph serves them as they grow.
-// (In a graph, 32 query and 8 key heads of 128, bf16: 16 x 1000 tokens 12.4 us in
-// parts, 15.9 shared evenly; 1 x 8000 10.6 and 15.9; 64 x 8000 167 and 170; 32 x 4000
-// 45.8 and 51.7.)
 //
 // A wave takes 32 tokens at a time, without LDS: the codes go from memory to
 // registers in the layout in which the matrix instructions (16x16x32, f16, fp32
@@ -757,24 +754,28 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args A, int64_t groups) 
 int pitch_of(int64_t dim) { return (int)((dim + 63) / 64 * 64); }
 int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
-// How a launch is cut. Lines in parts of at most kChunk tokens where that is
-// enough to keep the GPU busy, or the lines are many: a table's room is what the
-// host knows, and short sequences leave parts without work, but none waits
-// for a look at all lengths. Else the units shared evenly.
+// How a launch is cut: 256 lines or more are left whole, fewer go into about 512
+// parts, unless parts would be longer than kChunk tokens; then the units are shared
+// evenly. A table's room is what the host knows: parts of short sequences are
+// without work, but none waits for a look at all lengths. (32 query and 8 key heads
+// of 128, bf16, in a graph. 16 sequences of up to 2048 tokens: all of them full 18.8
+// us, spread evenly from 1 on 15.9, one full and the others of 100 tokens 11.6; in
+// 256 parts 18.6, 15.7, 14.4; shared evenly 20.4, 19.6, 9.9. 200 x 1000 tokens with
+// two key heads: whole 19.4, in 512 parts 24.2, shared evenly 31.2.)
 struct Cut {
   int64_t splits, chunk;  // splits 0: shared evenly
   int64_t groups;
 };
-constexpr int64_t kCuts = 256, kChunk = 4096;
+constexpr int64_t kEnough = 256, kParts = 512, kChunk = 4096;
 // Tokens that line_kernel's waves take at a time.
 int64_t step_of(int64_t dim) { return pitch_of(dim) > 128 ? 4 * kTile : 8 * kTile; }
-// most: tokens that a line may have. Parts are cut for fewer than 512 lines, into
-// fewer than 512 more: below kMaxSlots, as many as twice the even shares.
+// most: tokens that a line may have. Fewer than 256 lines are cut, into fewer than
+// 512 + 256 parts: below kMaxSlots, twice the even shares.
 constexpr int64_t kMaxSlots = 2 * kMaxGroups;
 Cut cut_of(int64_t batch, int64_t lines, int64_t dim, int64_t most) {
   const int64_t step = step_of(dim), steps = (most + step - 1) / step;
   if (steps <= 1) return {1, step, batch * lines};
-  int64_t splits = min64(steps, (kCuts + batch * lines - 1) / (batch * lines));
+  int64_t splits = batch * lines >= kEnough ? 1 : min64(steps, (kParts + batch * lines - 1) / (batch * lines));
   const int64_t chunk = (steps + splits - 1) / splits * step;
   splits = (most + chunk - 1) / chunk;
   if (chunk <= kChunk) return {splits, chunk, batch * lines * splits};
