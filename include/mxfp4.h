@@ -487,16 +487,17 @@ typedef struct {
  * in fp64, as mxfp4_rmsnorm), rounded to `dtype` once. eps < 0: no norm, then
  * the weights are NULL. q_weight, k_weight [dim] of weight_dtype (`dtype` or
  * fp32), NULL for 1. q_out [tokens][q heads][dim], k_out likewise. Either may
- * have no heads.
+ * have no heads. rstd [tokens][q heads + k heads] (NULL: not wanted; not written without a
+ * norm): 1 / sqrt(mean(x^2) + eps) of every head, which mxfp4_qk_norm_rope_bwd reads.
  */
 int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t tokens, int64_t dim,
                        int dtype, const mxfp4_rotation* rotation, const void* q_weight,
                        const void* k_weight, int weight_dtype, float eps, void* q_out, void* k_out,
-                       hipStream_t stream);
+                       float* rstd, hipStream_t stream);
 
 /*
  * mxfp4_qk_norm_rope_bwd -- gradients of mxfp4_qk_norm_rope. dq, dk: gradients
- * of its outputs; q, k: its inputs. With dz = dy turned back and g = dz weight:
+ * of its outputs; q, k: its inputs; rstd: as it wrote it (NULL: there was no norm). With dz = dy turned back and g = dz weight:
  * dx = r (g - u mean(g u)) to dq_out and dk_out (dense, in `dtype`; without a
  * norm dx = dz, and q and k are not read); dq_weight = sum over tokens and heads
  * of dz u, dk_weight likewise, in weight_dtype (NULL: not wanted; both of them
@@ -507,8 +508,9 @@ int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t token
 int mxfp4_qk_norm_rope_bwd(const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* q,
                            const mxfp4_heads* k, int64_t tokens, int64_t dim, int dtype,
                            const mxfp4_rotation* rotation, const void* q_weight, const void* k_weight,
-                           int weight_dtype, float eps, void* dq_out, void* dk_out, void* dq_weight,
-                           void* dk_weight, void* ws, size_t ws_bytes, hipStream_t stream);
+                           int weight_dtype, const float* rstd, void* dq_out, void* dk_out,
+                           void* dq_weight, void* dk_weight, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
 size_t mxfp4_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t k_heads,
                                               int64_t dim);
 

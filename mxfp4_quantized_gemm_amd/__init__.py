@@ -122,9 +122,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mxfp4_int8_gemm_workspace_bytes.argtypes = [i64, i64, i64]
     lib.mxfp4_int8_gemm_workspace_bytes.restype = sz
     heads, rot, kv = (ctypes.POINTER(t) for t in (Heads, Rotation, Int8KV))
-    lib.mxfp4_qk_norm_rope.argtypes = [heads, heads, i64, i64, i32, rot, p, p, i32, f32, p, p, p]
+    lib.mxfp4_qk_norm_rope.argtypes = [heads, heads, i64, i64, i32, rot, p, p, i32, f32, p, p, p, p]
     lib.mxfp4_qk_norm_rope.restype = i32
-    lib.mxfp4_qk_norm_rope_bwd.argtypes = [heads, heads, heads, heads, i64, i64, i32, rot, p, p, i32, f32, p, p, p,
+    lib.mxfp4_qk_norm_rope_bwd.argtypes = [heads, heads, heads, heads, i64, i64, i32, rot, p, p, i32, p, p, p, p,
                                            p, p, sz, p]
     lib.mxfp4_qk_norm_rope_bwd.restype = i32
     lib.mxfp4_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64]
@@ -746,21 +746,28 @@ def _kv(cache, device):
                   pages, heads, page, pitch)
 
 
-def mxfp4_qk_norm_rope(q, k, positions, frequencies, q_weight, k_weight, eps, q_out, k_out, axis_pairs=None,
+def _rstd(rstd, tokens, q, k, device):
+    import torch
+    return _dense(rstd, (tokens, q.size(1) + (0 if k is None else k.size(1))), torch.float32, "rstd", device)
+
+
+def mxfp4_qk_norm_rope(q, k, positions, frequencies, q_weight, k_weight, eps, q_out, k_out, rstd, axis_pairs=None,
                        interleaved=False, stream=None):
     """Norm (eps below 0: none) and rotation (frequencies None: none) of q and k into q_out and k_out
-    (k and k_out may be None)."""
+    (k and k_out, and rstd, may be None)."""
     tokens, _, dim = q.shape
     dtype, dev = q.dtype, q.device
     args = (_heads(q, tokens, dim, dtype, "q", dev), _heads(k, tokens, dim, dtype, "k", dev), tokens, dim, _dt(dtype),
             _rotation(positions, frequencies, axis_pairs, interleaved, tokens, dev),
-            *_head_weights(q_weight, k_weight, dim, dtype, dev), eps, _out(q, q_out, "q_out"), _out(k, k_out, "k_out"))
+            *_head_weights(q_weight, k_weight, dim, dtype, dev), eps, _out(q, q_out, "q_out"), _out(k, k_out, "k_out"),
+            _rstd(rstd, tokens, q, k, dev))
     _run(load_library().mxfp4_qk_norm_rope, args, dev, stream)
 
 
-def mxfp4_qk_norm_rope_bwd(dq, dk, q, k, positions, frequencies, q_weight, k_weight, eps, dq_out, dk_out, dq_weight,
+def mxfp4_qk_norm_rope_bwd(dq, dk, q, k, positions, frequencies, q_weight, k_weight, rstd, dq_out, dk_out, dq_weight,
                            dk_weight, ws, axis_pairs=None, interleaved=False, stream=None):
-    """Gradients of mxfp4_qk_norm_rope (the weights' and ws may be None; dk, k and dk_out too)."""
+    """Gradients of mxfp4_qk_norm_rope (rstd None: without a norm; the weights' and ws may be None; dk, k and
+    dk_out too)."""
     import torch
     tokens, _, dim = q.shape
     dtype, dev = q.dtype, q.device
@@ -773,8 +780,8 @@ def mxfp4_qk_norm_rope_bwd(dq, dk, q, k, positions, frequencies, q_weight, k_wei
         raise ValueError("dq and dk must have the shapes of q and k")
     args = (_heads(dq, tokens, dim, dtype, "dq", dev), _heads(dk, tokens, dim, dtype, "dk", dev),
             _heads(q, tokens, dim, dtype, "q", dev), _heads(k, tokens, dim, dtype, "k", dev), tokens, dim, _dt(dtype),
-            _rotation(positions, frequencies, axis_pairs, interleaved, tokens, dev), qw, kw, wt, eps,
-            _out(q, dq_out, "dq_out"), _out(k, dk_out, "dk_out"),
+            _rotation(positions, frequencies, axis_pairs, interleaved, tokens, dev), qw, kw, wt,
+            _rstd(rstd, tokens, q, k, dev), _out(q, dq_out, "dq_out"), _out(k, dk_out, "dk_out"),
             _dense(dq_weight, (dim,), type_of, "dq_weight", dev), _dense(dk_weight, (dim,), type_of, "dk_weight", dev),
             _vec(ws, 0, torch.uint8, "ws", dev), 0 if ws is None else ws.numel())
     _run(load_library().mxfp4_qk_norm_rope_bwd, args, dev, stream)

@@ -89,7 +89,7 @@ extern "C" {
 int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t tokens, int64_t dim,
                        int dtype, const mxfp4_rotation* rotation, const void* q_weight,
                        const void* k_weight, int weight_dtype, float eps, void* q_out, void* k_out,
-                       hipStream_t stream) {
+                       float* rstd, hipStream_t stream) {
   if (!q || !k) return MXFP4_ERR_NULL;
   int st = check_norm(dtype, weight_dtype, eps, q_weight, k_weight);
   if (st != MXFP4_OK) return st;
@@ -99,10 +99,12 @@ int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t token
   if (tokens == 0 || q->heads + k->heads == 0) return MXFP4_OK;
   if ((q->heads && (!q->p || !q_out)) || (k->heads && (!k->p || !k_out))) return MXFP4_ERR_NULL;
   const int s = size_of(dtype);
-  if (!aligned(q->p, s) || !aligned(k->p, s) || !aligned(q_out, s) || !aligned(k_out, s)) return MXFP4_ERR_ALIGN;
+  if (!aligned(q->p, s) || !aligned(k->p, s) || !aligned(q_out, s) || !aligned(k_out, s) ||
+      !aligned(rstd, 4))
+    return MXFP4_ERR_ALIGN;
   return hip_status(mx::launch_qk_norm_rope(heads_of(*q), heads_of(*k), tokens, dim, dtype, rot,
                                             norm_of(q_weight, k_weight, dtype, weight_dtype, eps), q_out, k_out,
-                                            stream));
+                                            eps >= 0.f ? rstd : nullptr, stream));
 }
 
 size_t mxfp4_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t k_heads,
@@ -113,12 +115,12 @@ size_t mxfp4_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int64_t q_heads, i
 int mxfp4_qk_norm_rope_bwd(const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* q,
                            const mxfp4_heads* k, int64_t tokens, int64_t dim, int dtype,
                            const mxfp4_rotation* rotation, const void* q_weight, const void* k_weight,
-                           int weight_dtype, float eps, void* dq_out, void* dk_out, void* dq_weight,
+                           int weight_dtype, const float* rstd, void* dq_out, void* dk_out, void* dq_weight,
                            void* dk_weight, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!dq || !dk || !q || !k) return MXFP4_ERR_NULL;
-  int st = check_norm(dtype, weight_dtype, eps, q_weight, k_weight);
+  const bool weights = dq_weight || dk_weight, norm = rstd != nullptr || tokens == 0;
+  int st = check_norm(dtype, weight_dtype, norm ? 0.f : -1.f, q_weight, k_weight);
   if (st != MXFP4_OK) return st;
-  const bool weights = dq_weight || dk_weight, norm = eps >= 0.f;
   if (weights && !norm) return MXFP4_ERR_MODE;
   if (!dim_ok(dim) || !tokens_ok(tokens) || !heads_ok(*q, tokens) || !heads_ok(*k, tokens) ||
       !heads_ok(*dq, tokens) || !heads_ok(*dk, tokens) || dq->heads != q->heads || dk->heads != k->heads)
@@ -135,11 +137,11 @@ int mxfp4_qk_norm_rope_bwd(const mxfp4_heads* dq, const mxfp4_heads* dk, const m
     if (weights && ws_bytes < mx::qk_norm_rope_bwd_ws(tokens, q->heads, k->heads, dim)) return MXFP4_ERR_WORKSPACE;
   }
   if (!aligned(q->p, s) || !aligned(k->p, s) || !aligned(dq->p, s) || !aligned(dk->p, s) || !aligned(dq_out, s) ||
-      !aligned(dk_out, s) || !aligned(ws, 4))
+      !aligned(dk_out, s) || !aligned(rstd, 4) || !aligned(ws, 4))
     return MXFP4_ERR_ALIGN;
   return hip_status(mx::launch_qk_norm_rope_bwd(
       heads_of(*dq), heads_of(*dk), heads_of(*q), heads_of(*k), tokens, dim, dtype, rot,
-      norm_of(q_weight, k_weight, dtype, weight_dtype, eps), dq_out, dk_out, dq_weight, dk_weight, ws, stream));
+      norm_of(q_weight, k_weight, dtype, weight_dtype, 0.f), rstd, dq_out, dk_out, dq_weight, dk_weight, ws, stream));
 }
 
 int mxfp4_int8_kv_write(const mxfp4_heads* q, const mxfp4_heads* k, const mxfp4_heads* v,

@@ -20,7 +20,7 @@ struct Heads {
   int64_t heads, ts, hs;
 };
 
-// The norm (eps < 0: none) and the weights of queries and keys (NULL: 1).
+// The norm (eps < 0: none; not looked at by the gradient) and the weights of queries and keys (NULL: 1).
 struct HeadNorm {
   const void *qw, *kw;
   bool wide;  // fp32 weights beside 16-bit heads
@@ -28,13 +28,13 @@ struct HeadNorm {
 };
 
 hipError_t launch_qk_norm_rope(Heads q, Heads k, int64_t tokens, int64_t dim, int dtype,
-                               const mxfp4_rotation& rot, HeadNorm n, void* qo, void* ko,
+                               const mxfp4_rotation& rot, HeadNorm n, void* qo, void* ko, float* rstd,
                                hipStream_t stream);
 // Gradients dx of q and k, and of the weights unless both are NULL (partial
-// sums in ws, qk_norm_rope_bwd_ws bytes).
+// sums in ws, qk_norm_rope_bwd_ws bytes). rstd NULL: no norm.
 hipError_t launch_qk_norm_rope_bwd(Heads dq, Heads dk, Heads q, Heads k, int64_t tokens, int64_t dim,
-                                   int dtype, const mxfp4_rotation& rot, HeadNorm n, void* dqx, void* dkx,
-                                   void* dqw, void* dkw, void* ws, hipStream_t stream);
+                                   int dtype, const mxfp4_rotation& rot, HeadNorm n, const float* rstd,
+                                   void* dqx, void* dkx, void* dqw, void* dkw, void* ws, hipStream_t stream);
 size_t qk_norm_rope_bwd_ws(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim);
 
 // Queries to qo, keys and values to the cache's slots; q.heads may be 0.

@@ -77,6 +77,21 @@ __device__ __forceinline__ void turn_table(const Angles& A, int64_t token, int n
   }
 }
 
+// The two weights as fp32 in LDS ([2][256], 1 where there is none), from where each row takes its
+// columns': kept in registers they cost 16 of each thread's. All threads.
+__device__ __forceinline__ void weight_table(const void* qw, const void* kw, int dim, int type, float* w) {
+  for (int c = threadIdx.x; c < dim; c += kThreads) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const void* p = k ? kw : qw;
+      w[k * (int)kHeadMax + c] = p == nullptr    ? 1.f
+                                 : type == kF32  ? get1<kF32>(p, c)
+                                 : type == kBF16 ? get1<kBF16>(p, c)
+                                                 : get1<kF16>(p, c);
+    }
+  }
+}
+
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -90,28 +105,68 @@ struct Lanes {
   typedef Row<T, EVEN, TPR, R> X;
   float c[R][V], s[R][V];  // the token's factors for these columns
 
-  // columns past the pairs keep their value: factors 1 and 0
-  __device__ __forceinline__ void factors(const float* cs, const float* sn, int rot, int t) {
+  // sign 1 to turn, -1 to turn back; columns past the pairs keep their value: factors 1 and 0
+  __device__ __forceinline__ void factors(const float* cs, const float* sn, int rot, float sign, int t) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int at = (t + TPR * i) * V + k;
         c[i][k] = at < rot ? cs[at] : 1.f;
-        s[i][k] = at < rot ? sn[at] : 0.f;
+        s[i][k] = at < rot ? sign * sn[at] : 0.f;
       }
   }
 
-  // z turned (sign 1) or turned back (sign -1). A pair's other value comes from
-  // the same thread (half 1), or through `meet`, which holds this row of the wave.
-  __device__ __forceinline__ void turn(float (&z)[R][V], float* meet, int half, int rot, float sign,
-                                       int t) const {
+  // A table's values of the columns (those past the row are not used).
+  static __device__ __forceinline__ void columns(const float* w, int t, float (&v)[R][V]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(w + (t + TPR * i) * V + k);
+        v[i][k] = f.x;
+        v[i][k + 1] = f.y;
+        v[i][k + 2] = f.z;
+        v[i][k + 3] = f.w;
+      }
+  }
+
+  // The value of the thread TPR / 2 away.
+  static __device__ __forceinline__ float opposite(float v, int t) {
+    const int b = __builtin_bit_cast(int, v);
+    if constexpr (TPR == 8) {  // from 4 above in the even fours, 4 below in the odd ones
+      const int a = __builtin_amdgcn_update_dpp(0, b, 0x104, 0xf, 0x5, false);
+      return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(a, b, 0x114, 0xf, 0xa, false));
+    } else if constexpr (TPR == 16) {  // rotated by 8
+      return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x128, 0xf, 0xf, false));
+    } else {
+      uint32_t lo, hi;
+      pair32<16>((uint32_t)b, lo, hi);
+      return __uint_as_float(t < 16 ? hi : lo);
+    }
+  }
+
+  // z turned. A pair's other value comes from
+  // the same thread (neighbours; fp32 halves of a whole row), from the thread opposite
+  // (16-bit halves of a whole row), or through `meet`, which holds this row of the wave.
+  __device__ __forceinline__ void turn(float (&z)[R][V], float* meet, int half, int rot, int t) const {
     float o[R][V];
+    // (a value, not a place: else the compiler chooses between z and LDS by address,
+    // and z goes to memory)
+    const auto value = [](float v) {
+      asm("" : "+v"(v));
+      return v;
+    };
     if (half == 1) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int k = 0; k < V; ++k) o[i][k] = z[i][k ^ 1];
+        for (int k = 0; k < V; ++k) o[i][k] = value(z[i][k ^ 1]);
+    } else if (half == TPR * kE / 2) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[i][k] = R == 2 ? value(z[R - 1 - i][k]) : opposite(z[i][k], t);
     } else {
       wave_sync();  // the last row's reads are done
 #pragma unroll
@@ -150,7 +205,7 @@ struct Lanes {
       for (int k = 0; k < V; ++k) {
         // an infinity behind the pairs is not multiplied by zero
         const int at = (t + TPR * i) * V + k;
-        z[i][k] = at < rot ? fmaf(z[i][k], c[i][k], sign * s[i][k] * o[i][k]) : z[i][k];
+        z[i][k] = at < rot ? fmaf(z[i][k], c[i][k], s[i][k] * o[i][k]) : z[i][k];
       }
   }
 };
@@ -171,12 +226,13 @@ __device__ __forceinline__ float factor(const float (&v)[R][V], double inv, floa
 struct HeadsArgs {
   Heads q, k, v;  // v.heads is 0 without a cache
   void *qo, *ko;
+  float* rstd;  // [tokens][q heads + k heads], or NULL
   const void *qw, *kw;
   Angles a;
   double inv_dim;
   int64_t first, tokens;  // of this launch: [first, tokens)
   int dim, rot;
-  int wpt;                // waves a token: 4, or 1
+  int tpg, parts;         // tokens a work-group: 4, 2, or 1 and it has one of `parts` of its heads
   float eps;
   bool norm, wide;
   // the cache: codes [pages][heads][page][pitch]
@@ -187,95 +243,147 @@ struct HeadsArgs {
   int page, pitch;
 };
 
+// A wave's rows at a time are of one kind (queries, keys or values): item i is
+// one of the queries', then of the keys', then of the values'.
+template <int RPW>
+struct Items {
+  int q, k, all;
+  __device__ __forceinline__ Items(const Heads& hq, const Heads& hk, int64_t v) {
+    q = ((int)hq.heads + RPW - 1) / RPW;
+    k = q + ((int)hk.heads + RPW - 1) / RPW;
+    all = k + ((int)v + RPW - 1) / RPW;
+  }
+  __device__ __forceinline__ int kind(int i) const { return i < q ? 0 : i < k ? 1 : 2; }
+  // head of the wave's row `sub`, which may be past the last
+  __device__ __forceinline__ int head(int i, int sub) const {
+    return (i - (i < q ? 0 : i < k ? q : k)) * RPW + sub;
+  }
+};
+
+// Loads first, what waits for them last: the first rows, the weights and the
+// slots are on their way while the token's cosines and sines are made, and a row's
+// loads while the one before is worked on. (8192 tokens of 32 + 8 heads of 128,
+// bf16: 32.6 us for 168 MB; without the latter, and with a pair's other value through LDS, 48.)
 template <int T, bool EVEN, int TPR, bool CACHE>
-__global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs A) {
+__global__ __launch_bounds__(kThreads, CACHE ? 6 : T == kF32 ? 7 : 8) void heads_kernel(HeadsArgs A) {
   typedef Lanes<T, EVEN, TPR> L;
   constexpr int R = L::R, V = L::V, RPW = 64 / TPR;
   __shared__ float cs[kWaves * kHeadMax], sn[kWaves * kHeadMax];
   __shared__ float meet_all[kWaves * 64 * kE];
-  __shared__ int64_t cell[kWaves];  // a token's row of head 0 in the cache, or -1
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, t = lane % TPR, sub = lane / TPR;
-  const int tpg = kWaves / A.wpt;   // tokens a work-group
-  const int64_t token0 = A.first + (int64_t)blockIdx.x * tpg;
-  const int n = (int)min((int64_t)tpg, A.tokens - token0);
-  turn_table(A.a, token0, n, cs, sn);
-  const int mine = wave / A.wpt;    // this wave's token of the work-group's
-  const int64_t token = token0 + mine;
+  __shared__ float weights[2 * kHeadMax];
+  __shared__ int again[kWaves];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, t = lane % TPR, sub = lane / TPR;
+  const int64_t group = blockIdx.x / A.parts;
+  const int part = blockIdx.x - (int)group * A.parts;
+  const int64_t token0 = A.first + group * A.tpg;
+  const int n = (int)min((int64_t)A.tpg, A.tokens - token0);
+  const int wpt = kWaves / A.tpg, mine = wave / wpt;  // waves a token; this wave's token of the work-group's
+  const int64_t token = token0 + (mine < n ? mine : 0);
+  const Items<RPW> items(A.q, A.k, A.v.heads);
+  int item = part * wpt + wave % wpt;
+  const int stride = wpt * A.parts;
+  // rows past the last of their kind are the last one's again, and not stored
+  const auto at = [&](int i) {
+    const int kind = items.kind(i);
+    const Heads& x = kind == 0 ? A.q : kind == 1 ? A.k : A.v;
+    return token * x.ts + min(items.head(i, sub), (int)x.heads - 1) * x.hs;
+  };
+  const auto from = [&](int i) { return i < items.q ? A.q.p : i < items.k ? A.k.p : A.v.p; };
+  u32x4 rows[R];  // the next ones
+  const auto load = [&](int i) {  // never under a condition, after which all loads would be waited for
+    i = min(i, items.all - 1);
+    if constexpr (EVEN) L::X::load_raw(from(i), at(i), A.dim, t, rows);
+  };
+  load(item);
+  if (A.norm) weight_table(A.qw, A.kw, A.dim, A.wide ? kF32 : T, weights);
+  int64_t cell = -1;  // the token's row of head 0 in the cache
   if constexpr (CACHE) {
-    // of tokens with the same slot the last one is written: work-groups look
-    // at the slots behind theirs (a launch has few tokens, see below)
+    // of tokens with the same slot the last one is written: work-groups look at the
+    // slots behind theirs (a launch has few tokens, see below), two a load, four loads at
+    // once; what a token without a slot finds does not matter
     int64_t slot[kWaves];
 #pragma unroll
+    for (int k = 0; k < kWaves; ++k) slot[k] = A.slots[token0 + min(k, n - 1)];
+    uint64_t same[kWaves] = {};
+    typedef int64_t i64x2 __attribute__((ext_vector_type(2), aligned(8)));
+    for (int64_t base = token0 + n; base < A.tokens; base += 8 * kThreads) {
+      i64x2 s[4];
+      bool both[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // past the end: the last token, with one before it that does not count
+        const int64_t i = base + 2 * (kThreads * e + (int)threadIdx.x);
+        both[e] = i < A.tokens - 1;
+        s[e] = *reinterpret_cast<const i64x2*>(A.slots + min(i, A.tokens - 2));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k)
+          same[k] |= __ballot(s[e].y == slot[k]) | __ballot(both[e] && s[e].x == slot[k]);
+    }
+    int found = 0;
+#pragma unroll
     for (int k = 0; k < kWaves; ++k) {
-      slot[k] = k < n ? A.slots[token0 + k] : -1;
-      if (slot[k] >= A.capacity) slot[k] = -1;
-    }
-    if (threadIdx.x < kWaves) {
-      int64_t at = -1;
+      found |= same[k] ? 1 << k : 0;
 #pragma unroll
-      for (int k = 0; k < kWaves; ++k)
-        if ((int)threadIdx.x == k && slot[k] >= 0) {
-          const uint32_t s = (uint32_t)slot[k], p = s / (uint32_t)A.page;
-          at = (int64_t)p * A.k.heads * A.page + (s - p * (uint32_t)A.page);
-        }
-      cell[threadIdx.x] = at;
+      for (int b = k + 1; b < kWaves; ++b) found |= b < n && slot[b] == slot[k] ? 1 << k : 0;
     }
-    __syncthreads();
-    for (int64_t i = token0 + 1 + threadIdx.x; i < A.tokens; i += kThreads) {
-      const int64_t s = A.slots[i];
+    if (lane == 0) again[wave] = found;
+    int64_t s = slot[0];
 #pragma unroll
-      for (int k = 0; k < kWaves; ++k)
-        if (s == slot[k] && i > token0 + k && s >= 0) cell[k] = -1;
+    for (int k = 1; k < kWaves; ++k) s = mine == k ? slot[k] : s;
+    if (s >= 0 && s < A.capacity) {
+      const uint32_t u = (uint32_t)s, p = u / (uint32_t)A.page;
+      cell = (int64_t)p * A.k.heads * A.page + (u - p * (uint32_t)A.page);
     }
   }
+  turn_table(A.a, token0, n, cs, sn);
   __syncthreads();
   if (mine >= n) return;  // no barrier of the work-group follows
+  if constexpr (CACHE) {
+    if ((again[0] | again[1] | again[2] | again[3]) >> mine & 1) cell = -1;
+  }
   L f;
   float* const meet = meet_all + (wave * 64 + sub * TPR) * kE;
-  f.factors(cs + mine * kHeadMax, sn + mine * kHeadMax, A.rot, t);
-  float qw[R][V], kw[R][V];
-  load_weight<T, EVEN, TPR, R>(A.qw, A.wide, A.dim, t, qw);
-  load_weight<T, EVEN, TPR, R>(A.kw, A.wide, A.dim, t, kw);
-  const int H = (int)A.q.heads, K = (int)A.k.heads, rows = H + K + (int)A.v.heads;
-  for (int g = (wave % A.wpt) * RPW; g < rows; g += A.wpt * RPW) {
-    // rows past the last are done again, and not stored
-    const int row = min(g + sub, rows - 1), kind = row < H ? 0 : row < H + K ? 1 : 2;
-    const int h = kind == 0 ? row : kind == 1 ? row - H : row - H - K;
-    const Heads& x = kind == 0 ? A.q : kind == 1 ? A.k : A.v;
+  f.factors(cs + mine * kHeadMax, sn + mine * kHeadMax, A.rot, 1.f, t);
+  for (; item < items.all; item += stride) {
     float v[R][V];
-    L::X::load(x.p, token * x.ts + h * x.hs, A.dim, t, v);
-    if (A.norm) {
-      const float r = factor<TPR>(v, A.inv_dim, A.eps);
+    if constexpr (EVEN) {
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-          v[i][k] = kind == 2 ? v[i][k] : v[i][k] * r * (kind == 0 ? qw[i][k] : kw[i][k]);
+      for (int i = 0; i < R; ++i) unpack<T, V>(rows[i], v[i]);
+      load(item + stride);
+    } else {
+      L::X::load(from(item), at(item), A.dim, t, v);
     }
-    if (A.rot > 0) {
-      float y[R][V];
+    const int kind = items.kind(item), h = items.head(item, sub);
+    const bool real = h < (int)(kind == 0 ? A.q.heads : A.k.heads);  // whole rows of threads
+    if (kind < 2) {
+      if (A.norm) {
+        float w[R][V];
+        L::columns(weights + kind * (int)kHeadMax, t, w);
+        const float r = factor<TPR>(v, A.inv_dim, A.eps);
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int k = 0; k < V; ++k) y[i][k] = v[i][k];
-      f.turn(y, meet, A.a.half, A.rot, 1.f, t);
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[i][k] = kind == 2 ? v[i][k] : y[i][k];
+          for (int k = 0; k < V; ++k) v[i][k] = v[i][k] * r * w[i][k];
+        if (!CACHE && A.rstd != nullptr && t == 0 && real)
+          A.rstd[token * (A.q.heads + A.k.heads) + (kind == 0 ? 0 : A.q.heads) + h] = r;
+      }
+      if (A.rot > 0) f.turn(v, meet, A.a.half, A.rot, t);
     }
-    if (g + sub >= rows) continue;  // whole rows of threads
+    if (!real) continue;
     if (kind == 0) {
-      L::X::store(A.qo, (token * H + h) * A.dim, A.dim, t, v);
+      L::X::store(A.qo, (token * A.q.heads + h) * A.dim, A.dim, t, v);
     } else if constexpr (CACHE) {
-      const int64_t at = cell[mine];
-      if (at >= 0) {
-        const int64_t to = at + (int64_t)h * A.page;
+      if (cell >= 0) {
+        const int64_t to = cell + (int64_t)h * A.page;
         write_codes<T, EVEN, TPR, R>(v, nullptr, (kind == 1 ? A.kc : A.vc) + to * A.pitch, A.pitch,
                                      (kind == 1 ? A.ks : A.vs) + to, A.dim, t);
       }
     } else {
-      L::X::store(A.ko, (token * K + h) * A.dim, A.dim, t, v);
+      L::X::store(A.ko, (token * A.k.heads + h) * A.dim, A.dim, t, v);
     }
   }
 }
@@ -284,13 +392,13 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs A) {
 struct HeadsBwdArgs {
   Heads q, k, dq, dk;
   void *qo, *ko;
+  const float* rstd;  // as the forward pass wrote them; NULL: no norm
   const void *qw, *kw;
   float* part;  // [gridDim.x][2][dim] partial sums of the weights' gradients, or NULL
   Angles a;
-  double inv_dim;
+  float inv_dim;
   int64_t tokens;
-  int dim, rot, wpt;
-  float eps;
+  int dim, rot, tpg, parts;
   bool norm, wide;
 };
 
@@ -298,58 +406,112 @@ struct HeadsBwdArgs {
 // registers, then over a work-group in LDS, then over work-groups by a second
 // kernel: a fixed order, no atomics.
 template <int T, bool EVEN, int TPR>
-__global__ __launch_bounds__(kThreads) void heads_bwd_kernel(HeadsBwdArgs A) {
+__global__ __launch_bounds__(kThreads, T == kF32 ? 3 : 4) void heads_bwd_kernel(HeadsBwdArgs A) {
   typedef Lanes<T, EVEN, TPR> L;
   constexpr int R = L::R, V = L::V, RPW = 64 / TPR;
   __shared__ float cs[kWaves * kHeadMax], sn[kWaves * kHeadMax];
   __shared__ float meet_all[kWaves * 64 * kE];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, t = lane % TPR, sub = lane / TPR;
-  const int tpg = kWaves / A.wpt, mine = wave / A.wpt;
-  const int H = (int)A.q.heads, rows = H + (int)A.k.heads;
+  __shared__ float weights[2 * kHeadMax];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, t = lane % TPR, sub = lane / TPR;
+  const int wpt = kWaves / A.tpg, mine = wave / wpt;
+  const Items<RPW> items(A.q, A.k, 0);
+  const int stride = wpt * A.parts;
   float* const meet = meet_all + (wave * 64 + sub * TPR) * kE;
-  float qw[R][V], kw[R][V], dqw[R][V] = {}, dkw[R][V] = {};
-  load_weight<T, EVEN, TPR, R>(A.qw, A.wide, A.dim, t, qw);
-  load_weight<T, EVEN, TPR, R>(A.kw, A.wide, A.dim, t, kw);
-  for (int64_t token0 = (int64_t)blockIdx.x * tpg; token0 < A.tokens; token0 += (int64_t)gridDim.x * tpg) {
-    const int n = (int)min((int64_t)tpg, A.tokens - token0);
+  float dqw[R][V] = {}, dkw[R][V] = {};
+  if (A.norm) weight_table(A.qw, A.kw, A.dim, A.wide ? kF32 : T, weights);
+  const int64_t groups = (A.tokens + A.tpg - 1) / A.tpg * A.parts;
+  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
+    const int64_t token0 = g / A.parts * A.tpg;
+    const int part = (int)(g % A.parts);
+    const int n = (int)min((int64_t)A.tpg, A.tokens - token0);
+    const int64_t token = token0 + (mine < n ? mine : 0);
+    int item = mine >= n ? items.all : part * wpt + wave % wpt;
+    const auto at = [&](const Heads& x, int i) {
+      return token * x.ts + min(items.head(i, sub), (int)x.heads - 1) * x.hs;
+    };
+    struct Next {  // rows that are on their way
+      u32x4 x[R], y[R];
+      float r;
+    } next[2];
+    const auto load = [&](int i, Next& to) {
+      i = min(i, items.all - 1);
+      const bool isq = i < items.q;
+      const Heads &x = isq ? A.q : A.k, &y = isq ? A.dq : A.dk;
+      if constexpr (EVEN) {
+        L::X::load_raw(y.p, at(y, i), A.dim, t, to.y);
+        if (A.norm) L::X::load_raw(x.p, at(x, i), A.dim, t, to.x);
+      }
+      if (A.norm)
+        to.r = A.rstd[token * (A.q.heads + A.k.heads) + (isq ? 0 : A.q.heads) +
+                      min(items.head(i, sub), (int)x.heads - 1)];
+    };
+    if (item < items.all) {
+      load(item, next[0]);
+      load(item + stride, next[1]);
+    }
     __syncthreads();  // the last tokens' factors are read
     turn_table(A.a, token0, n, cs, sn);
     __syncthreads();
-    if (mine >= n) continue;
-    const int64_t token = token0 + mine;
     L f;
-    f.factors(cs + mine * kHeadMax, sn + mine * kHeadMax, A.rot, t);
-    for (int g = (wave % A.wpt) * RPW; g < rows; g += A.wpt * RPW) {
-      const bool real = g + sub < rows;
-      const int row = min(g + sub, rows - 1);
-      const bool isq = row < H;
-      const int h = isq ? row : row - H;
-      const Heads &x = isq ? A.q : A.k, &y = isq ? A.dq : A.dk;
+    f.factors(cs + mine * kHeadMax, sn + mine * kHeadMax, A.rot, -1.f, t);
+    const auto work = [&](int item, Next& rows) {
+      const bool isq = item < items.q;
+      const int h = items.head(item, sub);
+      const bool real = h < (int)(isq ? A.q.heads : A.k.heads);
       float u[R][V], d[R][V];
-      L::X::load(y.p, token * y.ts + h * y.hs, A.dim, t, d);
-      if (A.norm) L::X::load(x.p, token * x.ts + h * x.hs, A.dim, t, u);
-      if (A.rot > 0) f.turn(d, meet, A.a.half, A.rot, -1.f, t);
-      if (A.norm) {
-        const float r = factor<TPR>(u, A.inv_dim, A.eps);
-        float s = 0.f;
+      const float r = rows.r;
+      if constexpr (EVEN) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) unpack<T, V>(rows.y[i], d[i]);
+        if (A.norm) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) unpack<T, V>(rows.x[i], u[i]);
+        }
+      } else {
+        const Heads &x = isq ? A.q : A.k, &y = isq ? A.dq : A.dk;
+        L::X::load(y.p, at(y, item), A.dim, t, d);
+        if (A.norm) L::X::load(x.p, at(x, item), A.dim, t, u);
+      }
+      load(item + 2 * stride, rows);
+      if (!real) {  // a row again: nothing for the weight
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            u[i][k] *= r;
-            const float e = d[i][k] * u[i][k];
-            dqw[i][k] += real && isq ? e : 0.f;
-            dkw[i][k] += real && !isq ? e : 0.f;
-            d[i][k] *= isq ? qw[i][k] : kw[i][k];
-            s = fmaf(d[i][k], u[i][k], s);
-          }
-        s = reduce_row<TPR>(s, (float*)nullptr, 0, add32) / (float)A.dim;
+          for (int k = 0; k < V; ++k) d[i][k] = 0.f;
+      }
+      if (A.rot > 0) f.turn(d, meet, A.a.half, A.rot, t);
+      if (A.norm) {
+        float s = 0.f, w[R][V];
+        L::columns(weights + (isq ? 0 : (int)kHeadMax), t, w);
+        const auto step = [&](float (&dw)[R][V]) {
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+              u[i][k] *= r;
+              dw[i][k] = fmaf(d[i][k], u[i][k], dw[i][k]);
+              d[i][k] *= w[i][k];
+              s = fmaf(d[i][k], u[i][k], s);
+            }
+        };
+        if (isq) {
+          step(dqw);
+        } else {
+          step(dkw);
+        }
+        s = reduce_row<TPR>(s, (float*)nullptr, 0, add32) * A.inv_dim;
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int k = 0; k < V; ++k) d[i][k] = r * (d[i][k] - u[i][k] * s);
       }
       if (real) L::X::store(isq ? A.qo : A.ko, (token * (isq ? A.q.heads : A.k.heads) + h) * A.dim, A.dim, t, d);
+    };
+    for (; item < items.all; item += 2 * stride) {
+      work(item, next[0]);
+      if (item + stride >= items.all) break;
+      work(item + stride, next[1]);
     }
   }
   if (A.part == nullptr) return;
@@ -371,27 +533,32 @@ __global__ __launch_bounds__(kThreads) void heads_bwd_kernel(HeadsBwdArgs A) {
 }
 
 // dw[c] = sum over the parts p of part[p][c], c < 2 dim (queries' weight, then
-// keys'): 32 half-waves of a work-group take every 32nd part of 32 columns.
+// keys'): 64 quarter-waves of a work-group take every 64th part of 16 columns.
 template <int T>
 __global__ __launch_bounds__(1024) void heads_dw_kernel(const float* part, int parts, int dim, void* dq,
                                                         void* dk) {
-  __shared__ float red[32][32];
-  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  __shared__ float red[64][17];
+  const int lane = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + lane;
   float s = 0.f;
   if (c < 2 * dim) {
-#pragma unroll 8
-    for (int p = q; p < parts; p += 32) s += part[(int64_t)p * 2 * dim + c];
+#pragma unroll 16
+    for (int p = q; p < parts; p += 64) s += part[(int64_t)p * 2 * dim + c];
   }
   red[q][lane] = s;
   __syncthreads();
-  if (q == 0 && c < 2 * dim) {
+  if (q < 4) {  // one wave: four sums of 16, then theirs
+    s = red[q][lane];
 #pragma unroll
-    for (int k = 1; k < 32; ++k) s += red[k][lane];
-    if (c < dim) {
-      if (dq != nullptr) put1<T>(dq, c, s);
-    } else if (dk != nullptr) {
-      put1<T>(dk, c - dim, s);
+    for (int k = 1; k < 16; ++k) s += red[q + 4 * k][lane];
+    s = far_lane<16>(s, add32);
+    s = far_lane<32>(s, add32);
+    if (q == 0 && c < 2 * dim) {
+      if (c < dim) {
+        if (dq != nullptr) put1<T>(dq, c, s);
+      } else if (dk != nullptr) {
+        put1<T>(dk, c - dim, s);
+      }
     }
   }
 }
@@ -406,42 +573,62 @@ struct ReadArgs {
   int dim, heads, page, pitch;
 };
 
-// y = code * scale, rounded once. A slot outside the cache reads as zeros.
-template <int T, bool EVEN, int TPR>
+// y = code * scale, rounded once. A slot outside the cache reads as zeros. (A code
+// is converted as the byte code + 128: a signed one's conversion takes three times as long.)
+template <int T, bool EVEN, int TPR, int ROWS>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs A) {
   constexpr int V = 16 / Type<T>::S, R = kE / V;
   const int t = threadIdx.x % TPR;
-  const int64_t rows = A.tokens * 2 * A.heads;
-  for (int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR; row < rows;
-       row += (int64_t)gridDim.x * (kThreads / TPR)) {
-    const int64_t token = row / (2 * A.heads);
-    const int at = (int)(row - token * 2 * A.heads), h = at >> 1;
-    const bool isv = at & 1;
-    const int64_t slot = A.slots[token];
-    float v[R][V] = {};
-    if (slot >= 0 && slot < A.capacity) {
-      const uint32_t s = (uint32_t)slot, p = s / (uint32_t)A.page;
-      const int64_t from = ((int64_t)p * A.heads + h) * A.page + (s - p * (uint32_t)A.page);
-      const float scale = (isv ? A.vs : A.ks)[from];
-      const uint8_t* q = (isv ? A.vc : A.kc) + from * A.pitch;
+  const uint32_t each = 2 * A.heads, rows = (uint32_t)A.tokens * each;  // below 2^31, see below
+  const uint32_t row0 = blockIdx.x * (ROWS * (kThreads / TPR)) + threadIdx.x / TPR;
+  // several rows a thread, all their slots and then all their codes on the way at once
+  int64_t slot[ROWS], to[ROWS];
+  uint32_t h[ROWS];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int c = (t + TPR * i) * V;
-        if (c < A.pitch) {  // the pitch is a multiple of 64: whole words
-          uint32_t d[V / 4];
-          if constexpr (V == 4) {
-            d[0] = *reinterpret_cast<const uint32_t*>(q + c);
-          } else {
-            const u32x2 e = *reinterpret_cast<const u32x2*>(q + c);
-            d[0] = e.x;
-            d[1] = e.y;
-          }
+  for (int n = 0; n < ROWS; ++n) {
+    const uint32_t row = min(row0 + n * (kThreads / TPR), rows - 1), token = row / each, at = row - token * each;
+    slot[n] = A.slots[token];
+    h[n] = at;
+    to[n] = ((int64_t)token * A.heads + (at >> 1)) * A.dim;
+  }
+  uint32_t d[ROWS][R][V / 4];
+  float scale[ROWS];
 #pragma unroll
-          for (int k = 0; k < V; ++k) v[i][k] = (float)(int8_t)(d[k / 4] >> (8 * (k & 3))) * scale;
-        }
+  for (int n = 0; n < ROWS; ++n) {
+    const bool in = slot[n] >= 0 && slot[n] < A.capacity;
+    const uint32_t s = in ? (uint32_t)slot[n] : 0, p = s / (uint32_t)A.page;
+    const int64_t from = ((int64_t)p * A.heads + (h[n] >> 1)) * A.page + (s - p * (uint32_t)A.page);
+    const uint8_t* q = (h[n] & 1 ? A.vc : A.kc) + from * A.pitch;
+    scale[n] = (h[n] & 1 ? A.vs : A.ks)[from];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = min((t + TPR * i) * V, A.pitch - V);  // the pitch is a multiple of 64: whole words
+      if constexpr (V == 4) {
+        d[n][i][0] = *reinterpret_cast<const uint32_t*>(q + c);
+      } else {
+        const u32x2 e = *reinterpret_cast<const u32x2*>(q + c);
+        d[n][i][0] = e.x;
+        d[n][i][1] = e.y;
       }
     }
-    Row<T, EVEN, TPR, R>::store(isv ? A.v : A.k, (token * A.heads + h) * A.dim, A.dim, t, v);
+    if (!in) {  // zeros, whatever the scale
+      scale[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) d[n][i][k] = 0;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < ROWS; ++n) {
+    if (row0 + n * (kThreads / TPR) >= rows) return;
+    float v[R][V];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        v[i][k] = ((float)((d[n][i][k / 4] ^ 0x80808080u) >> (8 * (k & 3)) & 255u) - 128.f) * scale[n];
+    Row<T, EVEN, TPR, R>::store(h[n] & 1 ? A.v : A.k, to[n], A.dim, t, v);
   }
 }
 
@@ -473,17 +660,32 @@ hipError_t by_type(int dtype, int64_t dim, F f) {
   }
 }
 
-// Waves a token: one where there are tokens enough to fill the GPU with a wave
-// each, else four share a token's heads.
-int waves_a_token(int64_t tokens) { return tokens >= 4096 ? 1 : 4; }
+// Work-groups: of as many tokens as leave about 2048 of them, which is how many
+// the GPU holds; below that one token each, or a part of its heads (a wave's rows at a
+// time for each wave) for up to 512 work-groups. A cache's work-group compares all slots
+// with its own whatever their number, and has four tokens already from 2048 on.
+// (32 + 8 heads of 128, bf16, one | four tokens each: 2048 tokens 13.0 | 14.4 us, with
+// the cache 18.1 | 17.1; 8192 tokens 40 | 32.6 us, with the cache 65 | 46.7.)
+struct Shape {
+  int tpg, parts;
+  int64_t groups;
+};
+Shape shape_of(int64_t tokens, int64_t heads, int64_t dim, bool cache = false) {
+  const int tpg = tokens >= (cache ? 2048 : 8192) ? 4 : tokens >= 4096 ? 2 : 1;
+  if (tpg > 1) return {tpg, 1, (tokens + tpg - 1) / tpg};
+  const int64_t rpw = dim <= 64 ? 8 : dim <= 128 ? 4 : 2, most = (heads + kWaves * rpw - 1) / (kWaves * rpw);
+  int64_t parts = tokens > 0 ? 512 / tokens : 1;
+  if (parts > most) parts = most;
+  if (parts < 1) parts = 1;
+  return {1, (int)parts, tokens * parts};
+}
 
 struct Forward {
   HeadsArgs A;
   hipStream_t st;
   template <int T, bool EVEN, int TPR>
   hipError_t go() const {
-    const int64_t tpg = kWaves / A.wpt;
-    const dim3 grid((unsigned)((A.tokens - A.first + tpg - 1) / tpg));
+    const dim3 grid((unsigned)((A.tokens - A.first + A.tpg - 1) / A.tpg * A.parts));
     if (A.slots)
       hipLaunchKernelGGL((heads_kernel<T, EVEN, TPR, true>), grid, dim3(kThreads), 0, st, A);
     else
@@ -508,16 +710,21 @@ struct Read {
   hipStream_t st;
   template <int T, bool EVEN, int TPR>
   hipError_t go() const {
+    // four rows a thread where that leaves work-groups for all CUs (32768 tokens of 8
+    // heads of 128, bf16: 38.7 us, 48 with one; 256 tokens: 3.0 us, 2.3 with one)
     const int64_t rows = A.tokens * 2 * A.heads, per = kThreads / TPR;
-    const int64_t groups = (rows + per - 1) / per;
-    hipLaunchKernelGGL((read_kernel<T, EVEN, TPR>), dim3((unsigned)(groups < 16384 ? groups : 16384)),
-                       dim3(kThreads), 0, st, A);
+    if (rows >= 2048 * per)
+      hipLaunchKernelGGL((read_kernel<T, EVEN, TPR, 4>), dim3((unsigned)((rows + 4 * per - 1) / (4 * per))),
+                         dim3(kThreads), 0, st, A);
+    else
+      hipLaunchKernelGGL((read_kernel<T, EVEN, TPR, 1>), dim3((unsigned)((rows + per - 1) / per)), dim3(kThreads), 0,
+                         st, A);
     return hipGetLastError();
   }
 };
 
 HeadsArgs forward_args(Heads q, Heads k, Heads v, int64_t tokens, int64_t dim, const mxfp4_rotation& rot,
-                       const HeadNorm& n, void* qo, void* ko) {
+                       const HeadNorm& n, void* qo, void* ko, const int64_t* slots) {
   HeadsArgs A{};
   A.q = q;
   A.k = k;
@@ -531,7 +738,10 @@ HeadsArgs forward_args(Heads q, Heads k, Heads v, int64_t tokens, int64_t dim, c
   A.tokens = tokens;
   A.dim = (int)dim;
   A.rot = 2 * (int)rot.pairs;
-  A.wpt = waves_a_token(tokens);
+  A.slots = slots;
+  const Shape sh = shape_of(tokens, q.heads + k.heads + v.heads, dim, slots != nullptr);
+  A.tpg = sh.tpg;
+  A.parts = sh.parts;
   A.eps = n.eps;
   A.norm = n.eps >= 0.f;
   A.wide = n.wide;
@@ -539,22 +749,23 @@ HeadsArgs forward_args(Heads q, Heads k, Heads v, int64_t tokens, int64_t dim, c
 }
 
 // A grid holds below 2^32 threads, and a launch of the cache's form looks at
-// the slots of all its tokens for each work-group's (32 KB, from the L2).
-constexpr int64_t kLaunchTokens = int64_t(1) << 22, kLaunchSlots = 4096;
+// the slots of all its tokens for each work-group's (64 KB at most, from the L2).
+constexpr int64_t kLaunchTokens = int64_t(1) << 22, kLaunchSlots = 8192;
 
 // Work-groups of the gradient: enough waves to keep the loads going, few
 // partial sums.
-int64_t bwd_groups(int64_t tokens) {
-  const int64_t tpg = kWaves / waves_a_token(tokens), need = (tokens + tpg - 1) / tpg;
+int64_t bwd_groups(int64_t tokens, int64_t heads, int64_t dim) {
+  const int64_t need = shape_of(tokens, heads, dim).groups;
   return need < 1024 ? need : 1024;
 }
 
 }  // namespace
 
 hipError_t launch_qk_norm_rope(Heads q, Heads k, int64_t tokens, int64_t dim, int dtype,
-                               const mxfp4_rotation& rot, HeadNorm n, void* qo, void* ko,
+                               const mxfp4_rotation& rot, HeadNorm n, void* qo, void* ko, float* rstd,
                                hipStream_t stream) {
-  HeadsArgs A = forward_args(q, k, Heads{}, tokens, dim, rot, n, qo, ko);
+  HeadsArgs A = forward_args(q, k, Heads{}, tokens, dim, rot, n, qo, ko, nullptr);
+  A.rstd = rstd;
   for (A.first = 0; A.first < tokens; A.first += kLaunchTokens) {
     A.tokens = tokens - A.first < kLaunchTokens ? tokens : A.first + kLaunchTokens;
     const hipError_t e = by_type(dtype, dim, Forward{A, stream});
@@ -566,12 +777,11 @@ hipError_t launch_qk_norm_rope(Heads q, Heads k, int64_t tokens, int64_t dim, in
 hipError_t launch_int8_kv_write(Heads q, Heads k, Heads v, int64_t tokens, int64_t dim, int dtype,
                                 const mxfp4_rotation& rot, HeadNorm n, const mxfp4_int8_kv& cache,
                                 const int64_t* slots, void* qo, hipStream_t stream) {
-  HeadsArgs A = forward_args(q, k, v, tokens, dim, rot, n, qo, nullptr);
+  HeadsArgs A = forward_args(q, k, v, tokens, dim, rot, n, qo, nullptr, slots);
   A.kc = static_cast<uint8_t*>(cache.k);
   A.vc = static_cast<uint8_t*>(cache.v);
   A.ks = cache.k_scales;
   A.vs = cache.v_scales;
-  A.slots = slots;
   A.capacity = cache.pages * cache.page_size;
   A.page = (int)cache.page_size;
   A.pitch = (int)cache.pitch;
@@ -585,16 +795,14 @@ hipError_t launch_int8_kv_write(Heads q, Heads k, Heads v, int64_t tokens, int64
 }
 
 size_t qk_norm_rope_bwd_ws(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim) {
-  (void)q_heads;
-  (void)k_heads;
-  return (size_t)bwd_groups(tokens) * 2 * (size_t)dim * sizeof(float);
+  return (size_t)bwd_groups(tokens, q_heads + k_heads, dim) * 2 * (size_t)dim * sizeof(float);
 }
 
 hipError_t launch_qk_norm_rope_bwd(Heads dq, Heads dk, Heads q, Heads k, int64_t tokens, int64_t dim,
-                                   int dtype, const mxfp4_rotation& rot, HeadNorm n, void* dqx, void* dkx,
-                                   void* dqw, void* dkw, void* ws, hipStream_t stream) {
+                                   int dtype, const mxfp4_rotation& rot, HeadNorm n, const float* rstd,
+                                   void* dqx, void* dkx, void* dqw, void* dkw, void* ws, hipStream_t stream) {
   const bool weights = dqw != nullptr || dkw != nullptr;
-  const int parts = (int)bwd_groups(tokens);
+  const int parts = (int)bwd_groups(tokens, q.heads + k.heads, dim);
   if (tokens > 0) {
     HeadsBwdArgs A{};
     A.q = q;
@@ -603,23 +811,25 @@ hipError_t launch_qk_norm_rope_bwd(Heads dq, Heads dk, Heads q, Heads k, int64_t
     A.dk = dk;
     A.qo = dqx;
     A.ko = dkx;
+    A.rstd = rstd;
     A.qw = n.qw;
     A.kw = n.kw;
     A.part = weights ? static_cast<float*>(ws) : nullptr;
     A.a = angles(rot, tokens);
-    A.inv_dim = 1.0 / (double)dim;
+    A.inv_dim = 1.f / (float)dim;
     A.tokens = tokens;
     A.dim = (int)dim;
     A.rot = 2 * (int)rot.pairs;
-    A.wpt = waves_a_token(tokens);
-    A.eps = n.eps;
-    A.norm = n.eps >= 0.f;
+    const Shape sh = shape_of(tokens, q.heads + k.heads, dim);
+    A.tpg = sh.tpg;
+    A.parts = sh.parts;
+    A.norm = rstd != nullptr;
     A.wide = n.wide;
     const hipError_t e = by_type(dtype, dim, Backward{A, (unsigned)parts, stream});
     if (e != hipSuccess) return e;
   }
   if (!weights) return hipSuccess;
-  const dim3 grid((unsigned)((2 * dim + 31) / 32)), blk(1024);
+  const dim3 grid((unsigned)((2 * dim + 15) / 16)), blk(1024);
   const float* p = static_cast<const float*>(ws);
   const int wt = n.wide ? kF32 : dtype;
   if (wt == kBF16)
@@ -633,10 +843,18 @@ hipError_t launch_qk_norm_rope_bwd(Heads dq, Heads dk, Heads q, Heads k, int64_t
 
 hipError_t launch_int8_kv_read(const mxfp4_int8_kv& cache, const int64_t* slots, int64_t tokens,
                                int64_t dim, int dtype, void* k, void* v, hipStream_t stream) {
-  const ReadArgs A{static_cast<const uint8_t*>(cache.k), static_cast<const uint8_t*>(cache.v),
-                   cache.k_scales, cache.v_scales, slots, k, v, tokens, cache.pages * cache.page_size,
-                   (int)dim, (int)cache.heads, (int)cache.page_size, (int)cache.pitch};
-  return by_type(dtype, dim, Read{A, stream});
+  // launches of below 2^27 rows, whose 32 threads each fit a grid
+  const int64_t most = (int64_t(1) << 27) / (2 * cache.heads), row = cache.heads * dim * (dtype == kF32 ? 4 : 2);
+  for (int64_t first = 0; first < tokens; first += most) {
+    const int64_t n = tokens - first < most ? tokens - first : most;
+    const ReadArgs A{static_cast<const uint8_t*>(cache.k), static_cast<const uint8_t*>(cache.v),
+                     cache.k_scales, cache.v_scales, slots + first, static_cast<uint8_t*>(k) + first * row,
+                     static_cast<uint8_t*>(v) + first * row, n, cache.pages * cache.page_size,
+                     (int)dim, (int)cache.heads, (int)cache.page_size, (int)cache.pitch};
+    const hipError_t e = by_type(dtype, dim, Read{A, stream});
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace mx

@@ -116,6 +116,16 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 q, int n) {
 template <int T, bool EVEN, int TPR, int R>
 struct Row {
   static constexpr int S = Type<T>::S, V = 16 / S;
+  // The chunks as they lie in memory (EVEN), for a row that is wanted later.
+  static __device__ __forceinline__ void load_raw(const void* p, int64_t row0, int cols, int t, u32x4 (&q)[R]) {
+    static_assert(EVEN, "chunks of odd rows are shifted");
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (t + TPR * i) * V;
+      q[i] = u32x4{0, 0, 0, 0};
+      if (c < cols) q[i] = *reinterpret_cast<const u32x4_2*>(static_cast<const uint8_t*>(p) + (row0 + c) * S);
+    }
+  }
   static __device__ __forceinline__ void load(const void* p, int64_t row0, int cols, int t,
                                               float (&v)[R][V]) {
 #pragma unroll

@@ -126,8 +126,9 @@ struct Turn {
   bool interleaved;
 };
 
+// (q', k'), and the heads' factors where `rstd` is given and there is a norm.
 std::pair<Tensor, Tensor> turn_forward(const Tensor& q, const Tensor& k, const Maybe& qw, const Maybe& kw,
-                                       const Turn& u) {
+                                       const Turn& u, Tensor* rstd) {
   on_gpu(q, "q");
   const int dtype = dtype_of(q, "q");
   const HeadRows rq = heads_of(q, "q");
@@ -137,8 +138,13 @@ std::pair<Tensor, Tensor> turn_forward(const Tensor& q, const Tensor& k, const M
   const HeadRows rk = heads_of(k, "k");
   const Rotation rot = rotation_of(u.positions, u.frequencies, u.sections, u.interleaved, tokens_of(q), rq.dim, q);
   const Tensor qo = dense_like(q), ko = dense_like(k);
+  float* r = nullptr;
+  if (rstd != nullptr && u.eps.has_value()) {
+    *rstd = at::empty({rq.tokens, rq.h.heads + rk.h.heads}, q.options().dtype(at::kFloat));
+    r = rstd->data_ptr<float>();
+  }
   check(mxfp4_qk_norm_rope(&rq.h, &rk.h, rq.tokens, rq.dim, dtype, &rot.r, n.qw, n.kw, n.type, n.eps, qo.data_ptr(),
-                           ko.data_ptr(), stream_of(q)),
+                           ko.data_ptr(), r, stream_of(q)),
         "mxfp4_qk_norm_rope");
   return {qo, ko};
 }
@@ -146,9 +152,11 @@ std::pair<Tensor, Tensor> turn_forward(const Tensor& q, const Tensor& k, const M
 struct TurnFunction : torch::autograd::Function<TurnFunction> {
   static variable_list forward(AutogradContext* ctx, const Tensor& q, const Tensor& k, const Maybe& qw,
                                const Maybe& kw, const Turn& u) {
-    const auto o = turn_forward(q, k, qw, kw, u);
+    Tensor rstd;
+    const auto o = turn_forward(q, k, qw, kw, u, &rstd);
     ctx->set_materialize_grads(false);
-    ctx->save_for_backward({q, k, has(qw) ? *qw : Tensor(), has(kw) ? *kw : Tensor(), u.positions, u.frequencies});
+    ctx->save_for_backward(
+        {q, k, has(qw) ? *qw : Tensor(), has(kw) ? *kw : Tensor(), u.positions, u.frequencies, rstd});
     ctx->saved_data["eps"] = u.eps.has_value() ? c10::IValue(*u.eps) : c10::IValue();
     ctx->saved_data["sections"] = u.sections.has_value() ? c10::IValue(*u.sections) : c10::IValue();
     ctx->saved_data["interleaved"] = u.interleaved;
@@ -168,6 +176,7 @@ struct TurnFunction : torch::autograd::Function<TurnFunction> {
     const bool want_qw = qw.defined() && ctx->needs_input_grad(2),
                want_kw = kw.defined() && ctx->needs_input_grad(qw.defined() ? 3 : 2);
     const Tensor &dq = grads[0], &dk = grads[1];
+    Tensor rstd = saved[6];
     no_tangent("the gradient of qk_norm_rope", {&dq, &dk});
     const c10::DeviceGuard guard(q.device());
     HeadRows rq = heads_of(q, "q"), rk = heads_of(k, "k"), rdq{}, rdk{};
@@ -176,6 +185,8 @@ struct TurnFunction : torch::autograd::Function<TurnFunction> {
     const Rotation rot =
         rotation_of(u.positions, u.frequencies, u.sections, u.interleaved, tokens_of(q), rq.dim, q);
     // an output that no loss reads has no heads here, and its input no gradient
+    if (rstd.defined() && dq.defined() != dk.defined())
+      rstd = (dq.defined() ? rstd.narrow(1, 0, rq.h.heads) : rstd.narrow(1, rq.h.heads, rk.h.heads)).contiguous();
     Tensor dqx, dkx, dqw, dkw, ws;
     if (dq.defined()) {
       rdq = heads_of(dq, "dq");
@@ -198,8 +209,8 @@ struct TurnFunction : torch::autograd::Function<TurnFunction> {
       ws = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
     }
     const int st = mxfp4_qk_norm_rope_bwd(&rdq.h, &rdk.h, &rq.h, &rk.h, rq.tokens, rq.dim, dtype_of(q, "q"), &rot.r,
-                                          n.qw, n.kw, n.type, n.eps, out(dqx), out(dkx), out(dqw), out(dkw), out(ws),
-                                          bytes, stream_of(q));
+                                          n.qw, n.kw, n.type, rstd.defined() ? rstd.const_data_ptr<float>() : nullptr,
+                                          out(dqx), out(dkx), out(dqw), out(dkw), out(ws), bytes, stream_of(q));
     TORCH_CHECK(st == MXFP4_OK, "mxfp4_qk_norm_rope_bwd: ", mxfp4_status_string(st), " (", st, ")");
     return {dqx, dkx, dqw, dkw, Tensor()};
   }
@@ -217,7 +228,7 @@ py::tuple qk_norm_rope(const Tensor& q, const Tensor& k, const Tensor& positions
     const variable_list o = TurnFunction::apply(q, k, qw, kw, u);
     return py::make_tuple(o[0], o[1]);
   }
-  const auto o = turn_forward(q, k, qw, kw, u);
+  const auto o = turn_forward(q, k, qw, kw, u, nullptr);
   return py::make_tuple(o.first, o.second);
 }
 

@@ -21,14 +21,14 @@ static int64_t g_q_heads;
 
 namespace mx {
 hipError_t launch_qk_norm_rope(Heads q, Heads, int64_t, int64_t, int, const mxfp4_rotation& rot, HeadNorm, void*,
-                               void*, hipStream_t) {
+                               void*, float*, hipStream_t) {
   ++g_launches;
   g_rot = rot;
   g_q_heads = q.heads;
   return g_result;
 }
 hipError_t launch_qk_norm_rope_bwd(Heads, Heads, Heads, Heads, int64_t, int64_t, int, const mxfp4_rotation& rot,
-                                   HeadNorm, void*, void*, void*, void*, void*, hipStream_t) {
+                                   HeadNorm, const float*, void*, void*, void*, void*, void*, hipStream_t) {
   ++g_launches;
   g_rot = rot;
   return g_result;
@@ -116,12 +116,12 @@ int main() {
   mxfp4_rotation r{(const int64_t*)p, (const double*)p, 32, 1, 0, {32, 0, 0, 0}};
   mxfp4_int8_kv c{p, (float*)p, p, (float*)p, 8, 4, 16, 64};
   // a launch for a good call, and its error handed on
-  CHECK(mxfp4_qk_norm_rope(&h, &h, 3, 64, 1, &r, p, p, 1, 1e-6f, p, p, nullptr) == MXFP4_OK && g_launches == 1);
+  CHECK(mxfp4_qk_norm_rope(&h, &h, 3, 64, 1, &r, p, p, 1, 1e-6f, p, p, nullptr, nullptr) == MXFP4_OK && g_launches == 1);
   CHECK(g_rot.pairs == 32 && g_q_heads == 4);
-  CHECK(mxfp4_qk_norm_rope(&h, &none, 3, 64, 1, nullptr, nullptr, nullptr, 1, -1.f, p, nullptr, nullptr) == MXFP4_OK);
+  CHECK(mxfp4_qk_norm_rope(&h, &none, 3, 64, 1, nullptr, nullptr, nullptr, 1, -1.f, p, nullptr, nullptr, nullptr) == MXFP4_OK);
   CHECK(g_launches == 2 && g_rot.pairs == 0 && g_rot.axes == 1);
   g_result = hipErrorInvalidValue;
-  CHECK(mxfp4_qk_norm_rope(&h, &h, 3, 64, 1, &r, p, p, 1, 1e-6f, p, p, nullptr) == MXFP4_ERR_HIP);
+  CHECK(mxfp4_qk_norm_rope(&h, &h, 3, 64, 1, &r, p, p, 1, 1e-6f, p, p, nullptr, nullptr) == MXFP4_ERR_HIP);
   CHECK(mxfp4_paged_attention(&h, 2, 64, 1, &c, (int32_t*)p, 4, 4, (int32_t*)p, 1.f, 0, p, nullptr, p, 1024, nullptr) ==
         MXFP4_OK + MXFP4_ERR_HIP);
   g_result = hipSuccess;
@@ -130,22 +130,22 @@ int main() {
   for (int64_t bad : {int64_t(-1), int64_t(1) << 62, INT64_MAX, INT64_MIN}) {
     mxfp4_heads x = h;
     x.token_stride = bad;
-    CHECK(mxfp4_qk_norm_rope(&x, &h, 3, 64, 1, &r, p, p, 1, 0.f, p, p, nullptr) == MXFP4_ERR_SHAPE);
+    CHECK(mxfp4_qk_norm_rope(&x, &h, 3, 64, 1, &r, p, p, 1, 0.f, p, p, nullptr, nullptr) == MXFP4_ERR_SHAPE);
     x = h;
     x.head_stride = bad;
-    CHECK(mxfp4_qk_norm_rope(&h, &x, 3, 64, 1, &r, p, p, 1, 0.f, p, p, nullptr) == MXFP4_ERR_SHAPE);
+    CHECK(mxfp4_qk_norm_rope(&h, &x, 3, 64, 1, &r, p, p, 1, 0.f, p, p, nullptr, nullptr) == MXFP4_ERR_SHAPE);
     x = h;
     x.heads = bad;
-    CHECK(mxfp4_qk_norm_rope(&h, &x, 3, 64, 1, &r, p, p, 1, 0.f, p, p, nullptr) == MXFP4_ERR_SHAPE);
-    CHECK(mxfp4_qk_norm_rope(&h, &h, bad, 64, 1, &r, p, p, 1, 0.f, p, p, nullptr) == MXFP4_ERR_SHAPE);
-    CHECK(mxfp4_qk_norm_rope(&h, &h, 3, bad, 1, &r, p, p, 1, 0.f, p, p, nullptr) == MXFP4_ERR_SHAPE);
+    CHECK(mxfp4_qk_norm_rope(&h, &x, 3, 64, 1, &r, p, p, 1, 0.f, p, p, nullptr, nullptr) == MXFP4_ERR_SHAPE);
+    CHECK(mxfp4_qk_norm_rope(&h, &h, bad, 64, 1, &r, p, p, 1, 0.f, p, p, nullptr, nullptr) == MXFP4_ERR_SHAPE);
+    CHECK(mxfp4_qk_norm_rope(&h, &h, 3, bad, 1, &r, p, p, 1, 0.f, p, p, nullptr, nullptr) == MXFP4_ERR_SHAPE);
     CHECK(mxfp4_int8_kv_read(&c, (int64_t*)p, bad, 64, 1, p, p, nullptr) == MXFP4_ERR_SHAPE);
     mxfp4_rotation t = r;
     t.pairs = bad;
-    CHECK(mxfp4_qk_norm_rope(&h, &h, 3, 64, 1, &t, p, p, 1, 0.f, p, p, nullptr) == MXFP4_ERR_SHAPE);
+    CHECK(mxfp4_qk_norm_rope(&h, &h, 3, 64, 1, &t, p, p, 1, 0.f, p, p, nullptr, nullptr) == MXFP4_ERR_SHAPE);
     t = r;
     t.axis_pairs[0] = bad;
-    CHECK(mxfp4_qk_norm_rope(&h, &h, 3, 64, 1, &t, p, p, 1, 0.f, p, p, nullptr) == MXFP4_ERR_SHAPE);
+    CHECK(mxfp4_qk_norm_rope(&h, &h, 3, 64, 1, &t, p, p, 1, 0.f, p, p, nullptr, nullptr) == MXFP4_ERR_SHAPE);
     mxfp4_int8_kv k = c;
     k.pages = bad;
     CHECK(mxfp4_int8_kv_read(&k, (int64_t*)p, 3, 64, 1, p, p, nullptr) == MXFP4_ERR_SHAPE);

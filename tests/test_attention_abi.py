@@ -42,12 +42,12 @@ def args(defaults, kw):
 
 def turn(lib, **kw):
     return lib.mxfp4_qk_norm_rope(*args(dict(q=heads(), k=heads(2), tokens=0 + 3, dim=64, dt=1, rot=rotation(), qw=P, kw=P,
-                                             wt=1, eps=1e-6, qo=P, ko=P), kw), None)
+                                             wt=1, eps=1e-6, qo=P, ko=P, rstd=P), kw), None)
 
 
 def turn_bwd(lib, **kw):
     a = dict(dq=heads(), dk=heads(2), q=heads(), k=heads(2), tokens=3, dim=64, dt=1, rot=rotation(), qw=P, kw=P, wt=1,
-             eps=1e-6, qo=P, ko=P, dqw=P, dkw=P, ws=P, wsb=lib.mxfp4_qk_norm_rope_bwd_workspace_bytes(3, 4, 2, 64))
+             rstd=P, qo=P, ko=P, dqw=P, dkw=P, ws=P, wsb=lib.mxfp4_qk_norm_rope_bwd_workspace_bytes(3, 4, 2, 64))
     return lib.mxfp4_qk_norm_rope_bwd(*args(a, kw), None)
 
 
@@ -66,9 +66,13 @@ def attend(lib, **kw):
 def check_shared(call, lib):
     assert call(lib, dt=3) == EMODE and call(lib, dt=-1) == EMODE
     assert call(lib, wt=2) == EMODE and call(lib, dt=0, wt=1) == EMODE
-    assert call(lib, eps=float("nan")) == EMODE
-    assert call(lib, eps=-1.0) == EMODE                        # weights without a norm
-    assert call(lib, eps=-1.0, qw=None) == EMODE
+    if call is turn_bwd:
+        assert call(lib, rstd=None) == EMODE                   # weights without a norm
+        assert call(lib, rstd=None, qw=None, dqw=None, dkw=None) == EMODE
+    else:
+        assert call(lib, eps=float("nan")) == EMODE
+        assert call(lib, eps=-1.0) == EMODE
+        assert call(lib, eps=-1.0, qw=None) == EMODE
     for dim in (0, -1, 257, 63):
         # 63: the rotation is wider than the head
         assert call(lib, dim=dim) == ESHAPE, dim
@@ -95,6 +99,7 @@ def check_shared(call, lib):
 
 def test_norm_rope_refusals(lib):
     check_shared(turn, lib)
+    assert turn(lib, rstd=TWO) == EALIGN
     assert turn(lib, q=None) == ENULL and turn(lib, k=None) == ENULL and turn(lib, ko=None) == ENULL
     assert turn(lib, tokens=0, q=heads(p=None), k=heads(p=None), qo=None, ko=None, rot=rotation(positions=None)) == OK
     assert turn(lib, q=heads(0, None), k=heads(0, None), qo=None, ko=None) == OK
@@ -111,8 +116,8 @@ def test_norm_rope_bwd_refusals(lib):
     assert turn_bwd(lib, dq=heads(3)) == ESHAPE and turn_bwd(lib, dk=heads(3)) == ESHAPE
     assert turn_bwd(lib, dq=heads(p=None)) == ENULL and turn_bwd(lib, dk=heads(2, p=None)) == ENULL
     assert turn_bwd(lib, ko=None) == ENULL
-    assert turn_bwd(lib, dqw=ODD) == EALIGN and turn_bwd(lib, ws=TWO) == EALIGN
-    assert turn_bwd(lib, eps=-1.0, qw=None, kw=None) == EMODE       # a weight's gradient without a norm
+    assert turn_bwd(lib, dqw=ODD) == EALIGN and turn_bwd(lib, ws=TWO) == EALIGN and turn_bwd(lib, rstd=TWO) == EALIGN
+    assert turn_bwd(lib, rstd=None, qw=None, kw=None) == EMODE       # a weight's gradient without a norm
     assert turn_bwd(lib, tokens=0, dqw=None, dkw=None, ws=None, wsb=0) == OK
     for k in ("dq", "dk", "q", "k"):
         assert turn_bwd(lib, **{k: None}) == ENULL

@@ -40,9 +40,10 @@ def distinct(T, capacity, seed):
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("T,heads,D,page", [(1, 1, 1, 16), (1, 8, 128, 64), (5, 2, 33, 16), (7, 3, 64, 48), (33, 2, 80, 32),
                                             (20, 4, 111, 16), (64, 2, 130, 64), (9, 1, 192, 16), (300, 3, 256, 128),
-                                            (4500, 2, 64, 64)])
+                                            (2051, 5, 96, 16),
+                                            (8203, 2, 64, 64)])
 def test_write_and_read(T, heads, D, page, dtype):
-    """From 4096 tokens on a wave has a token, and there are two launches."""
+    """Work-groups of one token, of four from 2048 on; launches of 8192."""
     from mxfp4_quantized_gemm_amd.int8 import int8_quantize
     from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_read, int8_kv_write
     dt = TYPES[dtype]
@@ -132,7 +133,7 @@ def test_slots_outside_the_cache():
         assert ((rk[i].float() - k[i].float()).abs() <= 0.51 * step + rk[i].float().abs() * 2.0 ** -8).all()
 
 
-@pytest.mark.parametrize("T", [2, 5, 300, 5000])
+@pytest.mark.parametrize("T", [2, 3, 5, 300, 2047, 5001, 8193, 17001])
 def test_the_last_of_equal_slots_stays(T):
     """Codes and scales of one token, whatever the launches."""
     from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_write

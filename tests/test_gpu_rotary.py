@@ -83,10 +83,10 @@ def test_widths(D, pairs, inter, dtype):
 
 
 @pytest.mark.parametrize("T,H,K", [(1, 1, 1), (1, 32, 8), (4, 1, 0), (3, 0, 2), (17, 9, 3), (130, 5, 5), (4097, 2, 1),
-                                   (5000, 3, 1)])
+                                   (5000, 3, 1), (8195, 1, 1)])
 @pytest.mark.parametrize("norm", [True, False])
 def test_tokens_and_heads(T, H, K, norm):
-    """One wave a token from 4096 tokens on, four below."""
+    """Work-groups of one token, of two from 4096 tokens on and of four from 8192."""
     check(case(T, H, K, 64, 32, "bf16", T + H, norm=norm))
 
 
@@ -280,10 +280,11 @@ def test_c_entry_points():
     pos, freq, dq, dk = gpu(c["pos"]), gpu(c["freq"]), gpu(c["dq"]), gpu(c["dk"])
     qo, ko, dqo, dko, dqw, dkw = (torch.full_like(t, 7) for t in (q, k, q, k, qw, kw))
     ws = torch.empty(mx.mxfp4_qk_norm_rope_bwd_workspace_bytes(20, 4, 2, 96), dtype=torch.uint8, device="cuda")
+    rstd = torch.empty(20, 6, device="cuda")
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
-    mx.mxfp4_qk_norm_rope(q, k, pos, freq, qw, kw, EPS, qo, ko, axis_pairs=(16, 24), stream=s)
-    mx.mxfp4_qk_norm_rope_bwd(dq, dk, q, k, pos, freq, qw, kw, EPS, dqo, dko, dqw, dkw, ws, axis_pairs=(16, 24), stream=s)
+    mx.mxfp4_qk_norm_rope(q, k, pos, freq, qw, kw, EPS, qo, ko, rstd, axis_pairs=(16, 24), stream=s)
+    mx.mxfp4_qk_norm_rope_bwd(dq, dk, q, k, pos, freq, qw, kw, rstd, dqo, dko, dqw, dkw, ws, axis_pairs=(16, 24), stream=s)
     s.synchronize()
     for got, ref in zip((qo, ko, dqo, dko, dqw, dkw), (*out, *want)):
         assert torch.equal(got, ref)
