@@ -487,8 +487,9 @@ typedef struct {
  * in fp64, as mxfp4_rmsnorm), rounded to `dtype` once. eps < 0: no norm, then
  * the weights are NULL. q_weight, k_weight [dim] of weight_dtype (`dtype` or
  * fp32), NULL for 1. q_out [tokens][q heads][dim], k_out likewise. Either may
- * have no heads. rstd [tokens][q heads + k heads] (NULL: not wanted; not written without a
- * norm): 1 / sqrt(mean(x^2) + eps) of every head, which mxfp4_qk_norm_rope_bwd reads.
+ * have no heads. rstd [tokens][q heads + k heads] (NULL: not wanted; not written
+ * without a norm): 1 / sqrt(mean(x^2) + eps) of every head, which
+ * mxfp4_qk_norm_rope_bwd reads.
  */
 int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t tokens, int64_t dim,
                        int dtype, const mxfp4_rotation* rotation, const void* q_weight,
@@ -497,8 +498,8 @@ int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t token
 
 /*
  * mxfp4_qk_norm_rope_bwd -- gradients of mxfp4_qk_norm_rope. dq, dk: gradients
- * of its outputs; q, k: its inputs; rstd: as it wrote it (NULL: there was no norm). With dz = dy turned back and g = dz weight:
- * dx = r (g - u mean(g u)) to dq_out and dk_out (dense, in `dtype`; without a
+ * of its outputs; q, k: its inputs; rstd: as it wrote it (NULL: there was no norm).
+ * With dz = dy turned back and g = dz weight: dx = r (g - u mean(g u)) to dq_out and dk_out (dense, in `dtype`; without a
  * norm dx = dz, and q and k are not read); dq_weight = sum over tokens and heads
  * of dz u, dk_weight likewise, in weight_dtype (NULL: not wanted; both of them
  * NULL without a norm; zeros where there are no tokens). Sums in fp32, in a
@@ -549,11 +550,12 @@ int mxfp4_int8_kv_read(const mxfp4_int8_kv* cache, const int64_t* slots, int64_t
  * 0, one past the table as the table's end. A sequence with no token
  * has out = 0 and lse = -infinity. Tokens of a page that is not in the cache
  * (pages[b][i] < 0 or >= pages) do not count; nothing past the length or
- * before the window does, whatever it holds. Sums in fp32, codes exact. Queries are held to
- * 2^-24 (bf16 and fp16: exact), or 2^-39 of a head's largest value; a probability
+ * before the window does, whatever it holds. Sums in fp32 (also that of the values,
+ * before its division by the sum of probabilities), codes exact. Queries are held
+ * to 2^-24 (bf16 and fp16: exact), or 2^-39 of a head's largest value; a probability
  * times its value's scale to 2^-12 for bf16 outputs and 2^-24 for others, or 2^-38 of
  * the largest such scale. An infinite scale that counts acts as NaN does.
- * table page_size <= 2^31 - 1024. ws: mxfp4_paged_attention_workspace_bytes
+ * table page_size <= 2^31 - 16384. ws: mxfp4_paged_attention_workspace_bytes
  * bytes, 4-byte aligned (may be 0, then ws may be NULL). Results do not depend on
  * the order in which work-groups run.
  */

@@ -75,11 +75,12 @@ int check_cache(const mxfp4_int8_kv* c, int64_t dim) {
   return MXFP4_OK;
 }
 
+// Positions in a table, and those up to two parts of a line behind its end, are 32-bit numbers.
 bool attention_sizes_ok(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t table,
                         int64_t page_size) {
   return tokens_ok(batch) && dim_ok(dim) && kv_heads >= 1 && q_heads >= 1 && q_heads <= mx::kHeadsMax &&
          q_heads % kv_heads == 0 && page_size >= mx::kPageUnit && page_size % mx::kPageUnit == 0 && table >= 0 &&
-         table <= (kMaxTokens - 1024) / page_size;
+         table <= (kMaxTokens - 16384) / page_size;
 }
 
 }  // namespace

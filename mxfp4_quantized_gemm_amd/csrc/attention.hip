@@ -10,14 +10,14 @@
 //
 // Work. A line is a key head of a sequence with up to 16 of its query heads. A
 // work-group takes a line, or a part of it of the same number of tokens for all
-// lines (line_kernel). Where parts would be
-// longer than 4096 tokens, and one long sequence among short ones would be waited for,
-// lines are cut into units of 128 tokens and the work-groups share the units of all
-// lines evenly, whatever the sequences' lengths (attention_kernel): work-group w takes
-// units [w U / W, (w + 1) U / W) of all U, in order of sequence, line and token. A line that
-// one work-group has whole is written by it; of the others every work-group
-// leaves maximum, sum and output in the workspace, and a second kernel joins them. The
-// lengths stay on the GPU: a captured graph serves them as they grow.
+// lines (line_kernel). Where parts would be longer than 4096 tokens, and one long
+// sequence among short ones would be waited for, lines are cut into units of 128
+// tokens and the work-groups share the units of all lines evenly, whatever the
+// sequences' lengths (attention_kernel): work-group w takes units [w U / W, (w + 1) U
+// / W) of all U, in order of sequence, line and token. A line that one work-group has
+// whole is written by it; of the others every work-group leaves maximum, sum and
+// output in the workspace, and a second kernel joins them. The lengths stay on the
+// GPU: a captured graph serves them as they grow.
 //
 // A wave takes 32 tokens at a time, without LDS: the codes go from memory to
 // registers in the layout in which the matrix instructions (16x16x32, f16, fp32
@@ -329,7 +329,8 @@ struct Wave {
 #pragma unroll
         for (int k = 0; k < 8; k += V) {
           float e[V];
-          unpack<T, V>(*reinterpret_cast<const u32x4_2*>(static_cast<const uint8_t*>(A.q.p) + (at + from + k) * Type<T>::S), e);
+          const uint8_t* p = static_cast<const uint8_t*>(A.q.p) + (at + from + k) * Type<T>::S;
+          unpack<T, V>(*reinterpret_cast<const u32x4_2*>(p), e);
 #pragma unroll
           for (int j = 0; j < V; ++j) v[s][k + j] = e[j];
         }
@@ -394,7 +395,8 @@ struct Wave {
 #pragma unroll
       for (int i = 0; i < DP / 64; ++i) {
         const int at = 64 * i + lane;
-        *reinterpret_cast<u32x4*>(stage + (16 * h + at / (DP / 16)) * kPitch<DP> + at % (DP / 16) * 16) = r.k[h][i] ^ kFlip;
+        uint8_t* const to = stage + (16 * h + at / (DP / 16)) * kPitch<DP> + at % (DP / 16) * 16;
+        *reinterpret_cast<u32x4*>(to) = r.k[h][i] ^ kFlip;
       }
     float* const scales = reinterpret_cast<float*>(stage + kTile * kPitch<DP>);
     scales[lane] = r.scale;
@@ -410,7 +412,8 @@ struct Wave {
     for (int i = 0; i < DP / 64; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        codes[h][i] = *reinterpret_cast<const u32x4*>(stage + (16 * h + (lane & 15)) * kPitch<DP> + (g + 4 * i) * 16);
+        codes[h][i] =
+            *reinterpret_cast<const u32x4*>(stage + (16 * h + (lane & 15)) * kPitch<DP> + (g + 4 * i) * 16);
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       Frag f[2];
@@ -503,7 +506,8 @@ struct Wave {
                                       int end, const Span& sp, float (&v)[KS][8], int lane) {
     constexpr int BUFS = AHEAD + 1, BATCH = 32 / BUFS * BUFS;
     Raw<DP> r[BUFS];
-    int left = t < end ? uniform((int)((uint32_t)(end - t + step - 1) / (uint32_t)step)) : 0;  // from the batch's first on
+    // tiles from the batch's first on
+    int left = t < end ? uniform((int)((uint32_t)(end - t + step - 1) / (uint32_t)step)) : 0;
     Places then = p;
     Rows16 now = rows_of_pages(A, p, head);
 #pragma unroll
@@ -546,8 +550,8 @@ __device__ __forceinline__ void finish(const Args& A, int64_t row, int d, float 
 // The waves' sums of a line meet in LDS: its output, or (part not NULL) the sums
 // for another kernel to join. `u` is in a wave's registers until here.
 template <int T, int DP, int NW, class W>
-__device__ __forceinline__ void meet(const Args& A, Shared<DP, NW>& lds, const W& u, int wave, int lane, int b, int head0, int heads,
-                                     float* part) {
+__device__ __forceinline__ void meet(const Args& A, Shared<DP, NW>& lds, const W& u, int wave, int lane, int b,
+                                     int head0, int heads, float* part) {
   auto& all = lds.all;
   __syncthreads();  // the waves are done with what they staged
   __shared__ float all_m[NW][kGroup], all_l[NW][kGroup];
@@ -754,27 +758,28 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args A, int64_t groups) 
 int pitch_of(int64_t dim) { return (int)((dim + 63) / 64 * 64); }
 int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
-// How a launch is cut: 256 lines or more are left whole, fewer go into about 512
-// parts, unless parts would be longer than kChunk tokens; then the units are shared
-// evenly. A table's room is what the host knows: parts of short sequences are
-// without work, but none waits for a look at all lengths. (32 query and 8 key heads
-// of 128, bf16, in a graph. 16 sequences of up to 2048 tokens: all of them full 18.8
-// us, spread evenly from 1 on 15.9, one full and the others of 100 tokens 11.6; in
-// 256 parts 18.6, 15.7, 14.4; shared evenly 20.4, 19.6, 9.9. 200 x 1000 tokens with
-// two key heads: whole 19.4, in 512 parts 24.2, shared evenly 31.2.)
+// How a launch is cut: 160 lines or more are left whole, and those of at most two
+// steps of a work-group's waves; others go into about 512 parts. Where work-groups would
+// have more than kChunk tokens, the units are shared evenly. A table's room is what
+// the host knows: parts of short sequences are without work, but none waits for a look
+// at all lengths. (32 query and 8 key heads of 128, bf16, in a graph. 16 sequences of
+// up to 2048 tokens: all of them full 18.8 us, spread evenly from 1 on 15.9, one full
+// and the others of 100 tokens 11.6; in 256 parts 18.6, 15.7, 14.4; shared evenly 20.4,
+// 19.6, 9.9. Whole | in parts: 20 x 1000 tokens 13.1 | 16.4, 30 x 4000 42.7 | 49.1, but
+// 16 x 4000 34.2 | 28.8; 1 x 500 7.6 | 8.3, but 1 x 1000 10.7 | 8.4.)
 struct Cut {
   int64_t splits, chunk;  // splits 0: shared evenly
   int64_t groups;
 };
-constexpr int64_t kEnough = 256, kParts = 512, kChunk = 4096;
+constexpr int64_t kEnough = 160, kParts = 512, kChunk = 4096;
 // Tokens that line_kernel's waves take at a time.
 int64_t step_of(int64_t dim) { return pitch_of(dim) > 128 ? 4 * kTile : 8 * kTile; }
-// most: tokens that a line may have. Fewer than 256 lines are cut, into fewer than
-// 512 + 256 parts: below kMaxSlots, twice the even shares.
+// most: tokens that a line may have. Fewer than 160 lines are cut, into fewer than
+// 512 + 160 parts: below kMaxSlots, twice the even shares.
 constexpr int64_t kMaxSlots = 2 * kMaxGroups;
 Cut cut_of(int64_t batch, int64_t lines, int64_t dim, int64_t most) {
   const int64_t step = step_of(dim), steps = (most + step - 1) / step;
-  if (steps <= 1) return {1, step, batch * lines};
+  if (steps <= 2) return {1, steps * step, batch * lines};
   int64_t splits = batch * lines >= kEnough ? 1 : min64(steps, (kParts + batch * lines - 1) / (batch * lines));
   const int64_t chunk = (steps + splits - 1) / splits * step;
   splits = (most + chunk - 1) / chunk;
@@ -819,7 +824,7 @@ hipError_t go_dim(const Args& A, hipStream_t st) {
 size_t paged_attention_ws(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t table,
                           int64_t page_size) {
   (void)batch;
-  if (table * page_size <= step_of(dim)) return 0;
+  if (table * page_size <= 2 * step_of(dim)) return 0;
   return (size_t)kMaxSlots * (size_t)min64(q_heads / kv_heads, kGroup) * (size_t)(pitch_of(dim) + 2) * sizeof(float);
 }
 

@@ -19,7 +19,7 @@ constexpr int kUnit = kTile * kUnitWaves;
 struct Span {
   int first, start, n, units;
 };
-// length: as given; most: what the table has room for (up to 2^31 - 1024);
+// length: as given; most: what the table has room for (up to 2^31 - 16384);
 // window: 0 for none.
 MX_HD Span span_of(int length, int most, int window) {
   Span s;

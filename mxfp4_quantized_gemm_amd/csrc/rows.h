@@ -150,13 +150,20 @@ struct Row {
         if (k < cols) v[0][k] = get1<T>(p, row0 + k);
     }
   }
+  // PAST: not to stay in the L2 (a streaming store).
+  template <bool PAST = false>
   static __device__ __forceinline__ void store(void* p, int64_t row0, int cols, int t,
                                                const float (&v)[R][V]) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int c = (t + TPR * i) * V;
-      if (EVEN ? c < cols : c + V <= cols)
-        *reinterpret_cast<u32x4_2*>(static_cast<uint8_t*>(p) + (row0 + c) * S) = pack<T, V>(v[i]);
+      u32x4_2* const to = reinterpret_cast<u32x4_2*>(static_cast<uint8_t*>(p) + (row0 + c) * S);
+      if (EVEN ? c < cols : c + V <= cols) {
+        if constexpr (PAST)
+          __builtin_nontemporal_store(pack<T, V>(v[i]), to);
+        else
+          *to = pack<T, V>(v[i]);
+      }
     }
     if (!EVEN && t == cols / V % TPR) {
       const int c = cols / V * V;

@@ -277,6 +277,12 @@ const int64_t* slots_of(const Tensor& slots, at::IntArrayRef lead, const Tensor&
   return slots.const_data_ptr<int64_t>();
 }
 
+// Autograd counts the changes of what it has saved (scales that a caller's graph reads, say).
+void written(const Cache& c) {
+  for (const Tensor* t : {&c.k, &c.ks, &c.v, &c.vs})
+    if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 void heads_like_cache(const Tensor& t, const char* name, const mxfp4_int8_kv& c) {
   TORCH_CHECK_VALUE(t.size(-2) == c.heads, name, " must have the cache's ", c.heads, " heads, got ", t.sizes());
 }
@@ -298,6 +304,7 @@ void int8_kv_write(const Tensor& k, const Tensor& v, const Tensor& ck, const Ten
   check(mxfp4_int8_kv_write(nullptr, &rk.h, &rv.h, rk.tokens, rk.dim, dtype, nullptr, nullptr, nullptr, dtype, -1.f,
                             &c, s, nullptr, stream_of(k)),
         "mxfp4_int8_kv_write");
+  written({ck, cks, cv, cvs});
 }
 
 Tensor int8_kv_append(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& ck, const Tensor& cks,
@@ -323,6 +330,7 @@ Tensor int8_kv_append(const Tensor& q, const Tensor& k, const Tensor& v, const T
   check(mxfp4_int8_kv_write(&rq.h, &rk.h, &rv.h, rq.tokens, rq.dim, dtype, &rot.r, n.qw, n.kw, n.type, n.eps, &c, s,
                             qo.data_ptr(), stream_of(q)),
         "mxfp4_int8_kv_write");
+  written({ck, cks, cv, cvs});
   return qo;
 }
 
@@ -436,6 +444,7 @@ py::tuple int8_attention(const Tensor& x, const Maybe& weight, double eps, const
   check(mxfp4_int8_kv_write(&q, &k, &v, B, dim, dtype, &rot.r, n.qw, n.kw, n.type, n.eps, &c, s, turned.data_ptr(),
                             stream_of(x)),
         "mxfp4_int8_kv_write");
+  written({ck, cks, cv, cvs});
   attend({turned.const_data_ptr(), H, H * dim, dim}, B, dim, dtype, c, t, scale, window, out, nullptr);
   const Tensor y = as(product(quantize(out, {}), o, os, {}, x.scalar_type()), x);
   return py::make_tuple(y, h.defined() ? h : x);

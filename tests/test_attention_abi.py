@@ -58,8 +58,8 @@ def write(lib, **kw):
 
 
 def attend(lib, **kw):
-    a = dict(q=heads(), batch=3, dim=64, dt=1, cache=cache(), pages=P, ld=20, table=20, lengths=P, scale=1.0, window=0,
-             out=P, lse=P, ws=P, wsb=lib.mxfp4_paged_attention_workspace_bytes(3, 4, 2, 64, 20, 16))
+    a = dict(q=heads(), batch=3, dim=64, dt=1, cache=cache(), pages=P, ld=40, table=40, lengths=P, scale=1.0, window=0,
+             out=P, lse=P, ws=P, wsb=lib.mxfp4_paged_attention_workspace_bytes(3, 4, 2, 64, 40, 16))
     return lib.mxfp4_paged_attention(*args(a, kw), None)
 
 
@@ -160,13 +160,14 @@ def test_paged_attention_refusals(lib):
     check_cache(attend, lib)
     assert attend(lib, dt=3) == EMODE
     for kw in (dict(dim=0), dict(dim=65), dict(batch=-1), dict(batch=1 << 31), dict(q=heads(3)), dict(q=heads(0)),
-               dict(q=heads(1026)), dict(ld=19), dict(ld=1 << 50), dict(table=-1), dict(window=-1),
-               dict(table=1 << 27, ld=1 << 27), dict(q=heads(ts=-1))):
+               dict(q=heads(1026)), dict(ld=39), dict(ld=1 << 50), dict(table=-1), dict(window=-1),
+               dict(table=1 << 27, ld=1 << 27), dict(q=heads(ts=-1)),
+               dict(table=(1 << 27) - 1023, ld=1 << 27)):
         assert attend(lib, **kw) == ESHAPE, kw
     for k in ("q", "lengths", "out", "pages", "ws"):
         assert attend(lib, **{k: None}) == ENULL, k
     assert attend(lib, q=heads(p=None)) == ENULL
-    need = lib.mxfp4_paged_attention_workspace_bytes(3, 4, 2, 64, 20, 16)
+    need = lib.mxfp4_paged_attention_workspace_bytes(3, 4, 2, 64, 40, 16)
     assert need > 0 and attend(lib, wsb=need - 1) == EWS
     for k in ("out", "pages", "lengths", "lse", "ws"):
         assert attend(lib, **{k: ODD}) == EALIGN, k

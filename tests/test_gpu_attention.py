@@ -62,7 +62,8 @@ def test_window(window):
 
 
 @pytest.mark.parametrize("lengths", [[9000], [70001, 3, 0, 500], [20] * 700, [0] * 5, list(range(1, 400, 3)),
-                                     [1] * 1500 + [4000, 0, 130]])
+                                     [1] * 1500 + [4000, 0, 130], [256], [257], [512, 3], [513, 511],
+                                     [600] * 79 + [1100], [600] * 80 + [1100]])
 def test_shares(lengths):
     """Lines cut over many work-groups, several in one, more sequences than a launch takes."""
     check(case(lengths, 2, 1, 64, 64, "fp32", len(lengths)))
@@ -220,6 +221,24 @@ def test_offsets_past_32_bits():
     assert torch.equal(paged_attention(q, big, where.int()[None].cuda(), n), a)
 
 
+def test_the_longest_table():
+    """A sequence of 2^31 - 16384 tokens, all of one page: its last ones are those of a short one."""
+    page, pages = 16, ((1 << 31) - 16384) // 16
+    cache = [t.cuda() for t in make_cache(1, 2, page, 64, 20)]
+    q = rand((1, 8, 64), torch.bfloat16, 20).cuda()
+    from mxfp4_quantized_gemm_amd.attention import paged_attention
+    far, short = (torch.zeros(1, n, dtype=torch.int32, device="cuda") for n in (pages, 400))
+    for window in (1, 100, 3000, 6000):
+        n = (window + 15) // 16 * 16  # the windows begin at the same row of a page
+        a = paged_attention(q, cache, far, torch.tensor([pages * page], dtype=torch.int32).cuda(), window=window)
+        b = paged_attention(q, cache, short, torch.tensor([n], dtype=torch.int32).cuda(), window=window)
+        assert torch.equal(a, b), window
+    from mxfp4_quantized_gemm_amd import MXFP4Error
+    with pytest.raises(MXFP4Error):
+        paged_attention(q, cache, torch.zeros(1, pages + 1, dtype=torch.int32, device="cuda"),
+                        torch.ones(1, dtype=torch.int32).cuda())
+
+
 def test_two_streams_at_once():
     c, d = case([3000, 10], 4, 2, 64, 16, "bf16", 15), case([4000, 50], 4, 2, 64, 16, "bf16", 16)
     want = [run(x)[0] for x in (c, d)]
@@ -306,6 +325,33 @@ def test_block_is_its_parts(H, KV, D, K, res):
     y3, h3 = step(w, x.view(5, 1, K), r.view(5, 1, K) if res else None, again, slots.view(5, 1), table, n,
                   torch.stack([pos, pos]).view(2, 5, 1), *args[4:], window=200, sections=(D // 4, D // 2 - D // 4))
     assert y3.shape == (5, 1, K) and torch.equal(y3.view(5, K), y) and torch.equal(h3.view(5, K), h)
+
+
+def test_block_of_no_sequence():
+    w = block(256, 4, 2, 64, 3)
+    cache = [t.cuda() for t in make_cache(4, 2, 16, 64, 1)]
+    before = [t.clone() for t in cache]
+    i64, i32 = (torch.zeros(0, dtype=d, device="cuda") for d in (torch.int64, torch.int32))
+    y, h = step(w, torch.zeros(0, 256, dtype=torch.bfloat16, device="cuda"), None, cache, i64, i32.view(0, 3), i32, i64,
+                frequencies(32).cuda(), 64)
+    assert y.shape == h.shape == (0, 256) and all(torch.equal(a, b) for a, b in zip(cache, before))
+
+
+def test_block_with_padding():
+    """Sequences with no slot and no length beside others: these as without them, nothing written for those."""
+    K, H, KV, D, page = 256, 4, 2, 64, 16
+    w = block(K, H, KV, D, 5)
+    cache = [t.cuda() for t in make_cache(12, KV, page, D, 1)]
+    table = torch.tensor([[3, 4, 5], [-1, -1, -1], [6, 7, 8]], dtype=torch.int32).cuda()
+    n = torch.tensor([20, 0, 48], dtype=torch.int32).cuda()
+    slots = torch.tensor([4 * page + 3, -1, 8 * page + 15]).cuda()
+    pos, freq = torch.tensor([19, 0, 47]).cuda(), frequencies(D // 2).cuda()
+    x = rand((3, K), torch.bfloat16, 1).cuda()
+    one, two = [t.clone() for t in cache], [t.clone() for t in cache]
+    y, _ = step(w, x, None, one, slots, table, n, pos, freq, D)
+    keep = torch.tensor([0, 2]).cuda()
+    y2, _ = step(w, x[keep], None, two, slots[keep], table[keep], n[keep], pos[keep], freq, D)
+    assert torch.equal(y[keep], y2) and not y[1].any() and all(torch.equal(a, b) for a, b in zip(one, two))
 
 
 def test_decoding_in_a_graph():

@@ -147,6 +147,22 @@ def test_the_last_of_equal_slots_stays(T):
     assert all(torch.equal(a, b) for a, b in zip(cache, once))
 
 
+def test_autograd_sees_the_write():
+    """A gradient whose saved scales a write has replaced is refused, as after torch's own changes."""
+    from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_append, int8_kv_write
+    x, slots = rand((2, 3, 64), torch.float32, 1).cuda(), torch.tensor([3, 40]).cuda()
+    for write in (lambda c: int8_kv_write(x, x, c, slots),
+                  lambda c: int8_kv_append(x, x, x, c, slots, slots, frequencies(32).cuda())):
+        cache = new_cache(4, 3, 64, 16)
+        w = torch.ones_like(cache.k_scales).requires_grad_(True)
+        y = (w * cache.k_scales).sum()
+        write(cache)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        with torch.inference_mode():
+            write(new_cache(4, 3, 64, 16))
+
+
 def test_rows_of_zeros_and_not_finite():
     from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_write
     k = rand((4, 1, 64), torch.float32, 1)
