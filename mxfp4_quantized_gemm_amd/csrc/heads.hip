@@ -266,7 +266,7 @@ struct Items {
 // Loads first, what waits for them last: the first rows, the weights and the
 // slots are on their way while the token's cosines and sines are made, and a row's
 // loads while the one before is worked on. (8192 tokens of 32 + 8 heads of 128,
-// bf16: 32.6 us for 168 MB; without the latter, and with a pair's other value through LDS, 48.)
+// bf16: 32 us for 168 MB; without the latter, and with a pair's other value through LDS, 48.)
 template <int T, bool EVEN, int TPR, bool CACHE>
 __global__ __launch_bounds__(kThreads, CACHE ? 6 : T == kF32 ? 7 : 8) void heads_kernel(HeadsArgs A) {
   typedef Lanes<T, EVEN, TPR> L;
@@ -668,15 +668,19 @@ hipError_t by_type(int dtype, int64_t dim, F f) {
 // Work-groups: of as many tokens as leave about 2048 of them, which is how many
 // the GPU holds; below that one token each, or a part of its heads (a wave's rows at a
 // time for each wave) for up to 512 work-groups. A cache's work-group compares all slots
-// with its own whatever their number, and has four tokens already from 2048 on.
-// (32 + 8 heads of 128, bf16, one | four tokens each: 2048 tokens 13.0 | 14.4 us, with
-// the cache 18.1 | 17.1; 8192 tokens 40 | 32.6 us, with the cache 65 | 46.7.)
+// with its own whatever their number, and has four tokens earlier, with few heads
+// earlier still. (32 + 8 heads of 128, bf16, one | two | four tokens each, us: 2048
+// tokens 11.4 | 11.4 | 13.2, with gradient 34.3 | 31.3 | 34.3, with the cache 17.5 | 14.9
+// | 17.2; 4096 tokens 19.6 | 16.7 | 18.0, with the cache 29.5 | 24.3 | 23.7; 8192 tokens
+// 38.8 | 34.7 | 33.4, with the cache 66.5 | 51.0 | 48.6; 3001 tokens of 5 heads of 96
+// written 15.1 | 10.9 | 9.4.)
 struct Shape {
   int tpg, parts;
   int64_t groups;
 };
 Shape shape_of(int64_t tokens, int64_t heads, int64_t dim, bool cache = false) {
-  const int tpg = tokens >= (cache ? 2048 : 8192) ? 4 : tokens >= 4096 ? 2 : 1;
+  const int64_t four = !cache ? 8192 : heads > 16 ? 4096 : 2048;
+  const int tpg = tokens >= four ? 4 : tokens >= 2048 ? 2 : 1;
   if (tpg > 1) return {tpg, 1, (tokens + tpg - 1) / tpg};
   const int64_t rpw = dim <= 64 ? 8 : dim <= 128 ? 4 : 2, most = (heads + kWaves * rpw - 1) / (kWaves * rpw);
   int64_t parts = tokens > 0 ? 512 / tokens : 1;

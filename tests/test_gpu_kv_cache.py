@@ -40,10 +40,10 @@ def distinct(T, capacity, seed):
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("T,heads,D,page", [(1, 1, 1, 16), (1, 8, 128, 64), (5, 2, 33, 16), (7, 3, 64, 48), (33, 2, 80, 32),
                                             (20, 4, 111, 16), (64, 2, 130, 64), (9, 1, 192, 16), (300, 3, 256, 128),
-                                            (2051, 5, 96, 16),
+                                            (2051, 5, 96, 16), (2049, 9, 48, 16),
                                             (8203, 2, 64, 64)])
 def test_write_and_read(T, heads, D, page, dtype):
-    """Work-groups of one token, of four from 2048 on; launches of 8192."""
+    """Work-groups of one token, of two or (up to 16 heads) four from 2048 on; launches of 8192."""
     from mxfp4_quantized_gemm_amd.int8 import int8_quantize
     from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_read, int8_kv_write
     dt = TYPES[dtype]

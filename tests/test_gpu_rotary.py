@@ -82,11 +82,11 @@ def test_widths(D, pairs, inter, dtype):
     check(case(5, 3, 2, D, pairs, dtype, 100 * D + pairs, interleaved=inter))
 
 
-@pytest.mark.parametrize("T,H,K", [(1, 1, 1), (1, 32, 8), (4, 1, 0), (3, 0, 2), (17, 9, 3), (130, 5, 5), (4097, 2, 1),
+@pytest.mark.parametrize("T,H,K", [(1, 1, 1), (1, 32, 8), (4, 1, 0), (3, 0, 2), (17, 9, 3), (130, 5, 5), (2049, 2, 1),
                                    (5000, 3, 1), (8195, 1, 1)])
 @pytest.mark.parametrize("norm", [True, False])
 def test_tokens_and_heads(T, H, K, norm):
-    """Work-groups of one token, of two from 4096 tokens on and of four from 8192."""
+    """Work-groups of one token, of two from 2048 tokens on and of four from 8192."""
     check(case(T, H, K, 64, 32, "bf16", T + H, norm=norm))
 
 
