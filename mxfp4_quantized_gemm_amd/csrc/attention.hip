@@ -39,9 +39,10 @@
 // value in [2^14, 2^15), and enter as one f16 number (bf16, fp16: exact but
 // for what lies 2^-39 below the largest) or as the sum of two (fp32: within 2^-24
 // of each, or 2^-39 of the largest). p vs is scaled by a power of two for the
-// largest vs so far, to below 2^14, and enters as one f16 number for bf16
-// outputs (2^-12 of each: an eighth of the output's own rounding), as the sum of
-// two for fp16 and fp32 (2^-24). All sums, the maximum and p are in fp32.
+// largest vs so far, to below 2^14, and enters as the sum of two (2^-24). One is enough
+// for bf16 outputs themselves (2^-12, and 64 x 4000 tokens take 85.9 us, not 89.2), but
+// the 8-bit product behind them rounds again: its result was twice as far from 64 bits
+// as with fp32 probabilities. All sums, the maximum and p are in fp32.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -258,9 +259,15 @@ __device__ __forceinline__ f32x4 mfma(const Frag& a, const Frag& b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v(), b.v(), c, 0, 0, 0);
 }
 
-// v as the sum of N f16 numbers, each the rest rounded to nearest.
+// v as the sum of N f16 numbers, each the rest rounded to nearest. (The values are hidden
+// from the compiler: it fuses a product that made one into its conversion, which can
+// then round otherwise than the fp32 number that the rest is taken from.)
 template <int N>
-__device__ __forceinline__ void split(const float (&v)[8], Frag (&f)[N]) {
+__device__ __forceinline__ void split(float (&v)[8], Frag (&f)[N]) {
+  if constexpr (N > 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) asm("" : "+v"(v[j]));
+  }
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const f16x2 h = {(_Float16)v[j], (_Float16)v[j + 1]};
@@ -300,9 +307,9 @@ union Shared {
 
 constexpr float kSmallest = 0x1p-112f;  // so that 2^14 over it is in fp32's range
 
-template <int T, int DP, int QP, int PP>
+template <int T, int DP, int QP>
 struct Wave {
-  static constexpr int KS = DP / 32, NB = DP / 16;
+  static constexpr int KS = DP / 32, NB = DP / 16, PP = 2;  // PP, QP: f16 numbers for p vs and a query
   Frag q[KS][QP];
   f32x4 acc[NB];  // sum of p vs c, times 2^14 / top_vs and 2^-9
   float hs;       // scores are sums of codes times this and ks
@@ -597,7 +604,7 @@ __device__ __forceinline__ void meet(const Args& A, Shared<DP, NW>& lds, const W
 }
 
 // Lines shared evenly by the work-groups.
-template <int T, int DP, int QP, int PP>
+template <int T, int DP, int QP>
 __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(Args A) {
   __shared__ int64_t prefix[kBatch + 1];
   __shared__ Shared<DP, kWaves> lds;
@@ -643,7 +650,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     const int t = uniform(sp.start + unit * kUnit + wave * kTile);
     const int end = uniform(min(sp.n, sp.start + (unit + count) * kUnit));
     const Places p = places(A, table, t, kUnit, lane);
-    typedef Wave<T, DP, QP, PP> Sums;
+    typedef Wave<T, DP, QP> Sums;
     Sums sums;
     sums.stage = lds.stage[wave];
     float q[Sums::KS][8];
@@ -657,7 +664,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
 }
 
 // A work-group a line, or one of A.splits parts of it, each of A.chunk tokens.
-template <int T, int DP, int QP, int PP, int NW>
+template <int T, int DP, int QP, int NW>
 __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : T == kF32 ? 2 : 4) void line_kernel(Args A) {
   __shared__ Shared<DP, NW> lds;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -667,7 +674,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : T == kF32 ? 2 : 4) void lin
   const int head0 = head * A.group + tile * kGroup, heads = min(A.group - tile * kGroup, kGroup);
   const int32_t* table = A.table + b * A.table_ld;
   const int length = A.lengths[b];
-  typedef Wave<T, DP, QP, PP> Sums;
+  typedef Wave<T, DP, QP> Sums;
   Sums sums;
   sums.stage = lds.stage[wave];
   float q[Sums::KS][8];
@@ -787,7 +794,7 @@ Cut cut_of(int64_t batch, int64_t lines, int64_t dim, int64_t most) {
   return {0, 0, min64(kMaxGroups, batch * lines * ((most + kUnit - 1) / kUnit))};
 }
 
-template <int T, int DP, int QP, int PP>
+template <int T, int DP, int QP>
 hipError_t go(Args A, hipStream_t st) {
   const Cut c = cut_of(A.batch, A.kv * A.tiles, A.dim, A.window > 0 ? min64(A.most, (int64_t)A.window + 15) : A.most);
   const dim3 heads((unsigned)(A.batch * A.q.heads));
@@ -796,12 +803,12 @@ hipError_t go(Args A, hipStream_t st) {
     A.splits = (int)c.splits;
     A.chunk = (int)c.chunk;
     constexpr int NW = DP > 128 ? 4 : 8;
-    hipLaunchKernelGGL((line_kernel<T, DP, QP, PP, NW>), dim3((unsigned)c.groups), dim3(64 * NW), 0, st, A);
+    hipLaunchKernelGGL((line_kernel<T, DP, QP, NW>), dim3((unsigned)c.groups), dim3(64 * NW), 0, st, A);
     e = hipGetLastError();
     if (e != hipSuccess || c.splits == 1) return e;
     hipLaunchKernelGGL((join_kernel<T, DP, true>), heads, dim3(kThreads), 0, st, A, c.groups);
   } else {
-    hipLaunchKernelGGL((attention_kernel<T, DP, QP, PP>), dim3((unsigned)c.groups), dim3(kThreads), 0, st, A);
+    hipLaunchKernelGGL((attention_kernel<T, DP, QP>), dim3((unsigned)c.groups), dim3(kThreads), 0, st, A);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((join_kernel<T, DP, false>), heads, dim3(kThreads), 0, st, A, c.groups);
@@ -809,13 +816,13 @@ hipError_t go(Args A, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int T, int QP, int PP>
+template <int T, int QP>
 hipError_t go_dim(const Args& A, hipStream_t st) {
   switch (pitch_of(A.dim)) {
-    case 64: return go<T, 64, QP, PP>(A, st);
-    case 128: return go<T, 128, QP, PP>(A, st);
-    case 192: return go<T, 192, QP, PP>(A, st);
-    default: return go<T, 256, QP, PP>(A, st);
+    case 64: return go<T, 64, QP>(A, st);
+    case 128: return go<T, 128, QP>(A, st);
+    case 192: return go<T, 192, QP>(A, st);
+    default: return go<T, 256, QP>(A, st);
   }
 }
 
@@ -858,9 +865,9 @@ hipError_t launch_paged_attention(Heads q, int64_t batch, int64_t dim, int dtype
     A.lse = lse ? lse + b * q.heads : nullptr;
     A.table = pages + b * pages_ld;
     A.lengths = lengths + b;
-    const hipError_t e = dtype == kBF16  ? go_dim<kBF16, 1, 1>(A, stream)
-                         : dtype == kF16 ? go_dim<kF16, 1, 2>(A, stream)
-                                         : go_dim<kF32, 2, 2>(A, stream);
+    const hipError_t e = dtype == kBF16  ? go_dim<kBF16, 1>(A, stream)
+                         : dtype == kF16 ? go_dim<kF16, 1>(A, stream)
+                                         : go_dim<kF32, 2>(A, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
