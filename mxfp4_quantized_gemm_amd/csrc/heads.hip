@@ -80,14 +80,17 @@ __device__ __forceinline__ void turn_table(const Angles& A, int64_t token, int n
   }
 }
 
-// The two weights as fp32 in LDS ([2][256], 1 where there is none), from where each row takes its
-// columns': kept in registers they cost 16 of each thread's. All threads.
+// The two weights as fp32 in LDS ([2][256], 1 where there is none), from where each row
+// takes its columns': kept in registers they cost 16 of each thread's. Zeros past the
+// head, for the threads whose columns those are: what lies in the LDS may be NaN, and
+// its product with their zeros would be. All threads.
 __device__ __forceinline__ void weight_table(const void* qw, const void* kw, int dim, int type, float* w) {
-  for (int c = threadIdx.x; c < dim; c += kThreads) {
+  for (int c = threadIdx.x; c < (int)kHeadMax; c += kThreads) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const void* p = k ? kw : qw;
-      w[k * (int)kHeadMax + c] = p == nullptr    ? 1.f
+      w[k * (int)kHeadMax + c] = c >= dim        ? 0.f
+                                 : p == nullptr  ? 1.f
                                  : type == kF32  ? get1<kF32>(p, c)
                                  : type == kBF16 ? get1<kBF16>(p, c)
                                                  : get1<kF16>(p, c);
@@ -120,7 +123,7 @@ struct Lanes {
       }
   }
 
-  // A table's values of the columns (those past the row are not used).
+  // A table's values of the columns, up to its 256.
   static __device__ __forceinline__ void columns(const float* w, int t, float (&v)[R][V]) {
 #pragma unroll
     for (int i = 0; i < R; ++i)

@@ -147,6 +147,24 @@ def test_the_last_of_equal_slots_stays(T):
     assert all(torch.equal(a, b) for a, b in zip(cache, once))
 
 
+@pytest.mark.parametrize("D", [2, 40, 80, 200])
+def test_narrow_heads_after_others_memory(D):
+    """What is left in the LDS by a call whose weights are all NaN changes no code or scale."""
+    from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_append
+    T, slots, pos = 600, torch.arange(600).cuda(), torch.arange(600).cuda()
+
+    def one(D, w):
+        x = rand((T, 8, D), torch.float32, D).cuda()
+        cache = new_cache(10, 8, D, 64)
+        w = torch.full((D,), w).cuda()
+        return int8_kv_append(x, x, x, cache, slots, pos, frequencies(D // 4).cuda(), w, w, 1e-6), *cache
+    want = one(D, 1.0)
+    for _ in range(4):
+        assert one(256, float("nan"))[0].isnan().all()
+        got = one(D, 1.0)
+        assert all(torch.equal(a, b) for a, b in zip(want, got)) and got[2].isfinite().all() and got[2].any()
+
+
 def test_autograd_sees_the_write():
     """A gradient whose saved scales a write has replaced is refused, as after torch's own changes."""
     from mxfp4_quantized_gemm_amd.kv_cache import int8_kv_append, int8_kv_write

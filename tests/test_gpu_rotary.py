@@ -82,6 +82,22 @@ def test_widths(D, pairs, inter, dtype):
     check(case(5, 3, 2, D, pairs, dtype, 100 * D + pairs, interleaved=inter))
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("D", [2, 40, 80, 200])
+def test_narrow_heads_after_others_memory(D, dtype):
+    """What is left in the LDS by a call whose weights are all NaN counts in no column past a head's width."""
+    bad = case(4096, 8, 8, 256, 128, dtype, 1)
+    bad["qw"].fill_(float("nan"))
+    bad["kw"].fill_(float("nan"))
+    args = [gpu(bad[n]) for n in ("q", "k", "qw", "kw")]
+    c = case(700, 5, 3, D, D // 4, dtype, D)
+    assert call(bad, *args)[0].isnan().all()
+    check(c)
+    leaves = [t.requires_grad_(True) for t in args]
+    torch.autograd.grad(call(bad, *leaves), leaves, (gpu(bad["dq"]), gpu(bad["dk"])))
+    check(c)
+
+
 @pytest.mark.parametrize("T,H,K", [(1, 1, 1), (1, 32, 8), (4, 1, 0), (3, 0, 2), (17, 9, 3), (130, 5, 5), (2049, 2, 1),
                                    (5000, 3, 1), (8195, 1, 1)])
 @pytest.mark.parametrize("norm", [True, False])
