@@ -24,5 +24,9 @@ def qk_norm_rope(q, k, positions, frequencies, q_weight=None, k_weight=None, eps
     (p, pairs + p), or (2 p, 2 p + 1) if interleaved. positions int64 [...],
     or with sections (pairs of each of up to four axes, as time, height and
     width) [axes, ...].
+
+    To capture a backward pass in a graph, keep no eager autograd graph of the same
+    leaves alive, as for any operator under torch: it would put the leaves'
+    accumulation on a stream that is not captured.
     """
     return ops.qk_norm_rope(q, k, positions, frequencies, q_weight, k_weight, eps, sections, interleaved)
