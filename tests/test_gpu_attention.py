@@ -70,6 +70,15 @@ def test_shares(lengths):
     check(case(lengths, 6, 2, 64, 16, "bf16", len(lengths) + 1))
 
 
+@pytest.mark.parametrize("H,K,D,dtype", [(40, 2, 64, "bf16"), (34, 2, 128, "fp16"), (4, 2, 256, "fp32"), (6, 2, 192, "bf16")])
+def test_shares_of_many_query_heads_and_wide_ones(H, K, D, dtype):
+    """Several tiles of query heads, and the widest heads, in equal parts and in shares, with a window too."""
+    check(case([3000, 70, 0], H, K, D, 16, dtype, 1))
+    c = case([5000] + [40, 0, 300] * 27, H, K, D, 64, dtype, 2)
+    check(c)
+    check(c, window=4500)
+
+
 @pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, 30.0])
 def test_scale(scale):
     """Flat, peaked (one token has all) and turned scores."""
