@@ -150,14 +150,18 @@ std::pair<Tensor, Tensor> turn_forward(const Tensor& q, const Tensor& k, const M
 }
 
 struct TurnFunction : torch::autograd::Function<TurnFunction> {
+  // Without a norm the gradient is dy turned back: the heads themselves are not kept, and may change.
   static variable_list forward(AutogradContext* ctx, const Tensor& q, const Tensor& k, const Maybe& qw,
                                const Maybe& kw, const Turn& u) {
     Tensor rstd;
     const auto o = turn_forward(q, k, qw, kw, u, &rstd);
+    const bool norm = u.eps.has_value();
     ctx->set_materialize_grads(false);
-    ctx->save_for_backward(
-        {q, k, has(qw) ? *qw : Tensor(), has(kw) ? *kw : Tensor(), u.positions, u.frequencies, rstd});
-    ctx->saved_data["eps"] = u.eps.has_value() ? c10::IValue(*u.eps) : c10::IValue();
+    ctx->save_for_backward({norm ? q : Tensor(), norm ? k : Tensor(), has(qw) ? *qw : Tensor(),
+                            has(kw) ? *kw : Tensor(), u.positions, u.frequencies, rstd});
+    ctx->saved_data["q_sizes"] = q.sizes().vec();
+    ctx->saved_data["k_sizes"] = k.sizes().vec();
+    ctx->saved_data["eps"] = norm ? c10::IValue(*u.eps) : c10::IValue();
     ctx->saved_data["sections"] = u.sections.has_value() ? c10::IValue(*u.sections) : c10::IValue();
     ctx->saved_data["interleaved"] = u.interleaved;
     return {o.first, o.second};
@@ -178,39 +182,44 @@ struct TurnFunction : torch::autograd::Function<TurnFunction> {
     const Tensor &dq = grads[0], &dk = grads[1];
     Tensor rstd = saved[6];
     no_tangent("the gradient of qk_norm_rope", {&dq, &dk});
-    const c10::DeviceGuard guard(q.device());
-    HeadRows rq = heads_of(q, "q"), rk = heads_of(k, "k"), rdq{}, rdk{};
+    if (!dq.defined() && !dk.defined())
+      return {Tensor(), Tensor(), want_qw ? at::zeros_like(qw) : Tensor(), want_kw ? at::zeros_like(kw) : Tensor(),
+              Tensor()};
+    const Tensor& like = dq.defined() ? dq : dk;
+    const c10::DeviceGuard guard(like.device());
+    const auto q_sizes = ctx->saved_data["q_sizes"].toIntVector(), k_sizes = ctx->saved_data["k_sizes"].toIntVector();
+    const at::IntArrayRef lead(q_sizes.data(), q_sizes.size() - 2);
+    const int64_t dim = q_sizes.back();
     const HeadNorm n = head_norm(qw.defined() ? Maybe(qw) : Maybe(), kw.defined() ? Maybe(kw) : Maybe(), u.eps,
-                                 rq.dim, q);
-    const Rotation rot =
-        rotation_of(u.positions, u.frequencies, u.sections, u.interleaved, tokens_of(q), rq.dim, q);
+                                 dim, like);
+    const Rotation rot = rotation_of(u.positions, u.frequencies, u.sections, u.interleaved, lead, dim, like);
     // an output that no loss reads has no heads here, and its input no gradient
-    if (rstd.defined() && dq.defined() != dk.defined())
-      rstd = (dq.defined() ? rstd.narrow(1, 0, rq.h.heads) : rstd.narrow(1, rq.h.heads, rk.h.heads)).contiguous();
+    HeadRows rq{}, rk{}, rdq{}, rdk{};
     Tensor dqx, dkx, dqw, dkw, ws;
-    if (dq.defined()) {
-      rdq = heads_of(dq, "dq");
-      dqx = dense_like(q);
-    } else {
-      rq.h.heads = 0;
-    }
-    if (dk.defined()) {
-      rdk = heads_of(dk, "dk");
-      dkx = dense_like(k);
-    } else {
-      rk.h.heads = 0;
-    }
+    const auto side = [&](const Tensor& x, const Tensor& dy, const std::vector<int64_t>& sizes, const char* name,
+                          HeadRows& rx, HeadRows& rdy, Tensor& dx) {
+      if (!dy.defined()) return;
+      rdy = heads_of(dy, name);
+      dx = at::empty(sizes, dy.options());
+      if (x.defined()) rx = heads_of(x, name);
+      rx.h.heads = rdy.h.heads;
+    };
+    side(q, dq, q_sizes, "q", rq, rdq, dqx);
+    side(k, dk, k_sizes, "k", rk, rdk, dkx);
+    const int64_t tokens = (dq.defined() ? rdq : rdk).tokens, heads = q_sizes[lead.size()];
+    if (rstd.defined() && dq.defined() != dk.defined())
+      rstd = (dq.defined() ? rstd.narrow(1, 0, heads) : rstd.narrow(1, heads, k_sizes[lead.size()])).contiguous();
     if (want_qw) dqw = dq.defined() ? at::empty_like(qw) : at::zeros_like(qw);
     if (want_kw) dkw = dk.defined() ? at::empty_like(kw) : at::zeros_like(kw);
     const auto out = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
     size_t bytes = 0;
     if (want_qw || want_kw) {
-      bytes = mxfp4_qk_norm_rope_bwd_workspace_bytes(rq.tokens, rq.h.heads, rk.h.heads, rq.dim);
-      ws = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
+      bytes = mxfp4_qk_norm_rope_bwd_workspace_bytes(tokens, rq.h.heads, rk.h.heads, dim);
+      ws = at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
     }
-    const int st = mxfp4_qk_norm_rope_bwd(&rdq.h, &rdk.h, &rq.h, &rk.h, rq.tokens, rq.dim, dtype_of(q, "q"), &rot.r,
+    const int st = mxfp4_qk_norm_rope_bwd(&rdq.h, &rdk.h, &rq.h, &rk.h, tokens, dim, dtype_of(like, "dq"), &rot.r,
                                           n.qw, n.kw, n.type, rstd.defined() ? rstd.const_data_ptr<float>() : nullptr,
-                                          out(dqx), out(dkx), out(dqw), out(dkw), out(ws), bytes, stream_of(q));
+                                          out(dqx), out(dkx), out(dqw), out(dkw), out(ws), bytes, stream_of(like));
     TORCH_CHECK(st == MXFP4_OK, "mxfp4_qk_norm_rope_bwd: ", mxfp4_status_string(st), " (", st, ")");
     return {dqx, dkx, dqw, dkw, Tensor()};
   }

@@ -15,7 +15,8 @@ from ._load import ops
 def qk_norm_rope(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=None, sections=None,
                  interleaved=False):
     """(q', k'), of the inputs' type; differentiable once in q, k and the
-    weights, in reverse mode (forward-mode tangents are refused).
+    weights, in reverse mode (forward-mode tangents are refused). Without a norm the
+    gradient needs neither q nor k: they are not kept for it, and may be overwritten.
 
     q [..., heads, dim] and k [..., key heads, dim], float32, bfloat16 or
     float16, any strides, dim up to 256. eps None: no norm, then no weights;
