@@ -498,11 +498,12 @@ int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t token
 
 /*
  * mxfp4_qk_norm_rope_bwd -- gradients of mxfp4_qk_norm_rope. dq, dk: gradients
- * of its outputs; q, k: its inputs; rstd: as it wrote it (NULL: there was no norm).
+ * of its outputs; q, k: its inputs; rstd: as it wrote it (NULL: there was no norm,
+ * or there are no heads).
  * With dz = dy turned back and g = dz weight: dx = r (g - u mean(g u)) to dq_out and dk_out (dense, in `dtype`; without a
  * norm dx = dz, and q and k are not read); dq_weight = sum over tokens and heads
  * of dz u, dk_weight likewise, in weight_dtype (NULL: not wanted; both of them
- * NULL without a norm; zeros where there are no tokens). Sums in fp32, in a
+ * NULL without a norm; zeros where there are no tokens or no heads). Sums in fp32, in a
  * fixed order. ws: mxfp4_qk_norm_rope_bwd_workspace_bytes bytes, 4-byte aligned
  * (NULL where both weights' gradients are).
  */

@@ -119,7 +119,8 @@ int mxfp4_qk_norm_rope_bwd(const mxfp4_heads* dq, const mxfp4_heads* dk, const m
                            int weight_dtype, const float* rstd, void* dq_out, void* dk_out, void* dq_weight,
                            void* dk_weight, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!dq || !dk || !q || !k) return MXFP4_ERR_NULL;
-  const bool weights = dq_weight || dk_weight, norm = rstd != nullptr || tokens == 0;
+  // (rstd has no values where there is no token or no head)
+  const bool weights = dq_weight || dk_weight, norm = rstd != nullptr || tokens == 0 || (q->heads == 0 && k->heads == 0);
   int st = check_norm(dtype, weight_dtype, norm ? 0.f : -1.f, q_weight, k_weight);
   if (st != MXFP4_OK) return st;
   if (weights && !norm) return MXFP4_ERR_MODE;

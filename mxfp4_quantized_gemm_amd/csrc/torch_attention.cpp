@@ -182,12 +182,15 @@ struct TurnFunction : torch::autograd::Function<TurnFunction> {
     const Tensor &dq = grads[0], &dk = grads[1];
     Tensor rstd = saved[6];
     no_tangent("the gradient of qk_norm_rope", {&dq, &dk});
-    if (!dq.defined() && !dk.defined())
-      return {Tensor(), Tensor(), want_qw ? at::zeros_like(qw) : Tensor(), want_kw ? at::zeros_like(kw) : Tensor(),
-              Tensor()};
+    const auto q_sizes = ctx->saved_data["q_sizes"].toIntVector(), k_sizes = ctx->saved_data["k_sizes"].toIntVector();
+    const auto has_heads = [](const Tensor& dy) { return dy.defined() && dy.size(-2) > 0; };
+    if (!has_heads(dq) && !has_heads(dk)) {
+      // nothing to turn back (and rstd has no values then, whose address would say that there was no norm)
+      const auto zeros = [](bool want, const Tensor& t) { return want ? at::zeros_like(t) : Tensor(); };
+      return {zeros(dq.defined(), dq), zeros(dk.defined(), dk), zeros(want_qw, qw), zeros(want_kw, kw), Tensor()};
+    }
     const Tensor& like = dq.defined() ? dq : dk;
     const c10::DeviceGuard guard(like.device());
-    const auto q_sizes = ctx->saved_data["q_sizes"].toIntVector(), k_sizes = ctx->saved_data["k_sizes"].toIntVector();
     const at::IntArrayRef lead(q_sizes.data(), q_sizes.size() - 2);
     const int64_t dim = q_sizes.back();
     const HeadNorm n = head_norm(qw.defined() ? Maybe(qw) : Maybe(), kw.defined() ? Maybe(kw) : Maybe(), u.eps,
