@@ -382,10 +382,12 @@ Tables tables_of(const Tensor& pages, const Tensor& lengths, int64_t batch, cons
   return t;
 }
 
+int64_t pitch_of(const Tables& t, int64_t batch) { return batch > 1 ? t.pages.stride(0) : t.pages.size(1); }
+
 // q.tokens sequences; out [sequences][heads][dim], dense.
 void attend(const mxfp4_heads& q, int64_t batch, int64_t dim, int dtype, const mxfp4_int8_kv& c, const Tables& t,
             std::optional<double> scale, int64_t window, const Tensor& out, float* lse) {
-  const int64_t table = t.pages.size(1), ld = batch > 1 ? t.pages.stride(0) : table;
+  const int64_t table = t.pages.size(1), ld = pitch_of(t, batch);
   const size_t bytes = mxfp4_paged_attention_workspace_bytes(batch, q.heads, c.heads, dim, table, c.page_size);
   Tensor ws;
   if (bytes) ws = at::empty({(int64_t)bytes}, out.options().dtype(at::kByte));
@@ -445,6 +447,12 @@ py::tuple int8_attention(const Tensor& x, const Maybe& weight, double eps, const
   const Tables t = tables_of(pages, lengths, slots.numel(), x);
   const c10::DeviceGuard guard(x.device());
   const Rotation rot = rotation_of(positions, frequencies, sections, interleaved, lead, dim, x);
+  // what the calls behind the write to the cache refuse (an attention of no sequence checks the sizes)
+  check_product(o, os, x, "out");
+  const mxfp4_heads none{nullptr, H, 0, 0};
+  check(mxfp4_paged_attention(&none, 0, dim, dtype, &c, nullptr, pitch_of(t, slots.numel()), t.pages.size(1), nullptr,
+                              1.f, window, nullptr, nullptr, nullptr, 0, nullptr),
+        "mxfp4_paged_attention");
   Tensor h;
   const Operand in = norm_int8(x, weight, eps, residual, &h);
   const Tensor mid = product(in, qkv, qkvs, {}, x.scalar_type());

@@ -110,6 +110,8 @@ Operand norm_int8(const Tensor& x, const Maybe& weight, double eps, const Maybe&
 Operand quantize(const Tensor& x, const Maybe& gate);
 Tensor product(const Operand& x, const Tensor& w, const Tensor& sw, const Maybe& bias, at::ScalarType out);
 void check_weight(const Tensor& w, int64_t cols, const char* name);
+// What product() refuses of a weight, for calls that change something before it.
+void check_product(const Tensor& w, const Tensor& sw, const Tensor& like, const char* name);
 Tensor as(const Tensor& y, const Tensor& x);  // y [rows][N] with x's leading dimensions
 
 void bind_attention(pybind11::module_& m);  // torch_attention.cpp

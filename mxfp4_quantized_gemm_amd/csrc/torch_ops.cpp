@@ -234,6 +234,16 @@ Tensor product(const Operand& x, const Tensor& w, const Tensor& sw, const Maybe&
   return gemm(x.codes, x.scales, w, sw, bias, w.size(1), out);
 }
 
+void check_product(const Tensor& w, const Tensor& sw, const Tensor& like, const char* name) {
+  int64_t ld;
+  const void* p = codes_of(w, w.size(1), name, &like, &ld);
+  const float* s = floats(sw, w.size(0), name, like);
+  // a product of no rows checks the sizes
+  check(mxfp4_int8_gemm(nullptr, padded(w.size(1)), nullptr, p, ld, s, nullptr, 0, w.size(0), w.size(1), nullptr,
+                        w.size(0), MXFP4_DT_F32, nullptr, 0, nullptr),
+        "mxfp4_int8_gemm");
+}
+
 void check_weight(const Tensor& w, int64_t cols, const char* name) {
   TORCH_CHECK_VALUE(w.dim() == 2 && (w.size(1) == cols || w.size(1) == padded(cols)), name, " must have ", cols,
                     " or ", padded(cols), " columns, got ", w.sizes());

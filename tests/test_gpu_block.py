@@ -1,5 +1,5 @@
 """The 8-bit attention block: every type, layout of pairs and scale against the public calls that it
-stands for, and in 32 bits against 64."""
+stands for, in 32 bits against 64, and refused calls that leave the cache as it was."""
 import pytest
 import torch
 
@@ -140,3 +140,23 @@ def test_against_64_bits(H, KV, D, K, scale, inter, seed):
         rows, scales = got[i].cpu()[at[0], :, at[2]], got[i + 1].cpu()[at[0], :, at[2]]
         assert torch.equal(rows[..., :D].double(), codes) and not rows[..., D:].any()
         near(scales, st, err, "scales")
+
+
+def test_a_refused_block_leaves_the_cache():
+    """What is wrong with the output product's weight or the page tables is said before anything is written."""
+    from mxfp4_quantized_gemm_amd import MXFP4Error
+    c = gpu(case(4, 2, 64, 256, [20, 3], "bf16", 11))
+    codes, scales = c["w"]["out"]
+    cache = [t.clone() for t in c["cache"]]
+    far = torch.zeros(1, 1, dtype=torch.int32, device="cuda").expand(2, ((1 << 31) - 16384) // PAGE + 1)
+    bad = [(dict(out=(codes, scales[:-1])), ValueError), (dict(out=(codes, scales.double())), TypeError),
+           (dict(out=(codes, scales.cpu())), ValueError), (dict(out=(codes.short(), scales)), TypeError),
+           (dict(out=(codes.cpu(), scales)), ValueError), (dict(out=(codes[:1].expand(256, -1), scales)), ValueError),
+           (dict(out=(torch.stack([codes, codes], -1)[..., 0], scales)), ValueError),
+           (dict(table=far), MXFP4Error), (dict(window=-1), ValueError)]
+    for i, (kw, error) in enumerate(bad):
+        with pytest.raises(error):
+            block(c, cache, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(cache, c["cache"])), i
+    block(c, cache)
+    assert not torch.equal(cache[0], c["cache"][0])
