@@ -95,8 +95,10 @@ struct HeadNorm {
 HeadNorm head_norm(const Maybe& qw, const Maybe& kw, std::optional<double> eps, int64_t dim, const Tensor& like) {
   HeadNorm n{nullptr, nullptr, dtype_of(like, "q"), -1.f};
   if (eps.has_value()) {
-    TORCH_CHECK_VALUE(*eps >= 0 && std::isfinite(*eps), "eps must be a number from 0 on, or None, got ", *eps);
     n.eps = (float)*eps;
+    // (one that fp32 has not would be infinity, and every result 0, or 0, and rows of zeros NaN)
+    TORCH_CHECK_VALUE(*eps >= 0 && std::isfinite(n.eps) && (n.eps > 0 || *eps == 0),
+                      "eps must be 0, a positive number in fp32's range, or None, got ", *eps);
   }
   TORCH_CHECK_VALUE(eps.has_value() || (!has(qw) && !has(kw)), "weights need a norm: eps is None");
   if (has(qw) && has(kw))
