@@ -18,10 +18,11 @@ bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) 
 int hip_status(hipError_t e) { return e == hipSuccess ? MXFP4_OK : MXFP4_ERR_HIP; }
 bool dim_ok(int64_t dim) { return dim >= 1 && dim <= mx::kHeadMax; }
 bool tokens_ok(int64_t tokens) { return tokens >= 0 && tokens < kMaxTokens; }
+bool count_ok(int64_t heads) { return heads >= 0 && heads <= mx::kHeadsMax; }
 
 // Strides whose last offset fits.
 bool heads_ok(const mxfp4_heads& x, int64_t tokens) {
-  return x.heads >= 0 && x.heads <= mx::kHeadsMax && x.token_stride >= 0 && x.head_stride >= 0 &&
+  return count_ok(x.heads) && x.token_stride >= 0 && x.head_stride >= 0 &&
          x.token_stride <= kMaxOffset / (tokens > 0 ? tokens : 1) && x.head_stride <= kMaxOffset / mx::kHeadsMax;
 }
 
@@ -110,7 +111,9 @@ int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t token
 
 size_t mxfp4_qk_norm_rope_bwd_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t k_heads,
                                               int64_t dim) {
-  return tokens_ok(tokens) && dim_ok(dim) ? mx::qk_norm_rope_bwd_ws(tokens, q_heads, k_heads, dim) : 0;
+  return tokens_ok(tokens) && dim_ok(dim) && count_ok(q_heads) && count_ok(k_heads)
+             ? mx::qk_norm_rope_bwd_ws(tokens, q_heads, k_heads, dim)
+             : 0;
 }
 
 int mxfp4_qk_norm_rope_bwd(const mxfp4_heads* dq, const mxfp4_heads* dk, const mxfp4_heads* q,
