@@ -301,10 +301,12 @@ __device__ __forceinline__ void wave_sync() {
 
 // A work-group's LDS: what its waves stage, then their sums.
 template <int DP, int NW>
-union Shared {
+union alignas(16) Shared {
   uint8_t stage[NW][kTile * kPitch<DP> + 256];
   float all[NW][kGroup][DP + 4];
 };
+
+static_assert(alignof(Shared<64, 4>) >= 16, "it is accessed 16 bytes at a time");
 
 constexpr float kSmallest = 0x1p-112f;  // so that 2^14 over it is in fp32's range
 

@@ -277,9 +277,10 @@ __global__ __launch_bounds__(kThreads, CACHE ? 6 : T == kF32 ? 7 : 8) void heads
   typedef Lanes<T, EVEN, TPR> L;
   constexpr int R = L::R, V = L::V, RPW = 64 / TPR;
   __shared__ float cs[kWaves * kHeadMax], sn[kWaves * kHeadMax];
-  __shared__ float meet_all[kWaves * 64 * kE];
-  __shared__ float weights[2 * kHeadMax];
+  alignas(16) __shared__ float meet_all[kWaves * 64 * kE];
+  alignas(16) __shared__ float weights[2 * kHeadMax];
   __shared__ int again[kWaves];
+  static_assert(__alignof__(meet_all) >= 16 && __alignof__(weights) >= 16, "they are accessed 16 bytes at a time");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, t = lane % TPR, sub = lane / TPR;
   const int64_t group = blockIdx.x / A.parts;
@@ -418,8 +419,9 @@ __global__ __launch_bounds__(kThreads, T == kF32 ? 3 : 4) void heads_bwd_kernel(
   typedef Lanes<T, EVEN, TPR> L;
   constexpr int R = L::R, V = L::V, RPW = 64 / TPR;
   __shared__ float cs[kWaves * kHeadMax], sn[kWaves * kHeadMax];
-  __shared__ float meet_all[kWaves * 64 * kE];
-  __shared__ float weights[2 * kHeadMax];
+  alignas(16) __shared__ float meet_all[kWaves * 64 * kE];
+  alignas(16) __shared__ float weights[2 * kHeadMax];
+  static_assert(__alignof__(meet_all) >= 16 && __alignof__(weights) >= 16, "they are accessed 16 bytes at a time");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, t = lane % TPR, sub = lane / TPR;
   const int wpt = kWaves / A.tpg, mine = wave / wpt;
