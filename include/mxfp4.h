@@ -554,7 +554,12 @@ int mxfp4_int8_kv_read(const mxfp4_int8_kv* cache, const int64_t* slots, int64_t
  * before the window does, whatever it holds. Sums in fp32 (also that of the values,
  * before its division by the sum of probabilities), codes exact. Queries are held
  * to 2^-24 (bf16 and fp16: exact), or 2^-39 of a head's largest value; a probability
- * times its value's scale to 2^-24, or 2^-38 of the largest such scale. An infinite scale that counts acts as NaN does.
+ * times its value's scale to 2^-24, or 2^-38 of the largest such scale.
+ * A key scale that is infinite makes a token's score infinite (NaN where q . k is
+ * 0), as an infinite query can. A score of -infinity is a probability of 0, and
+ * where all scores are, the result is that of a sequence with no token; one of
+ * +infinity or NaN makes out and lse NaN. An infinite or NaN value scale of a token
+ * that counts makes out NaN, whatever its probability.
  * table page_size <= 2^31 - 16384. ws: mxfp4_paged_attention_workspace_bytes
  * bytes, 4-byte aligned (may be 0, then ws may be NULL). Results do not depend on
  * the order in which work-groups run.

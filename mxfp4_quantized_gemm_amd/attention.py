@@ -20,7 +20,9 @@ def paged_attention(q, cache, pages, lengths, scale=None, window=0, return_lse=F
     Sequence b attends to its first lengths[b] tokens (int32), the last ``window``
     of them if window > 0; token t is row t % page_size of page
     pages[b][t // page_size] (int32). A sequence without tokens gives zeros;
-    tokens of a page that is not in the cache (-1, say) do not count.
+    tokens of a page that is not in the cache (-1, say) do not count. A score of
+    -infinity (of an infinite query or key scale) is a probability of 0, and a sequence
+    with no other gives zeros; one of +infinity or NaN gives NaN.
     scale: dim^-1/2 if None. return_lse: also the logarithm of the sum of the
     scores' exponentials, float32 [batch][heads].
     """
