@@ -484,7 +484,8 @@ typedef struct {
 /*
  * mxfp4_qk_norm_rope -- for every head x of q and of k: u = x / sqrt(mean(x^2)
  * + eps), z = u weight, and z turned by `rotation` (NULL: not), in fp32 (the mean
- * in fp64, as mxfp4_rmsnorm), rounded to `dtype` once. eps < 0: no norm, then
+ * in fp64, as mxfp4_rmsnorm; its factor in fp32, which a head of a root mean square
+ * below 2^-128 and no eps leaves), rounded to `dtype` once. eps < 0: no norm, then
  * the weights are NULL. q_weight, k_weight [dim] of weight_dtype (`dtype` or
  * fp32), NULL for 1. q_out [tokens][q heads][dim], k_out likewise. Either may
  * have no heads. rstd [tokens][q heads + k heads] (NULL: not wanted; not written
@@ -499,11 +500,11 @@ int mxfp4_qk_norm_rope(const mxfp4_heads* q, const mxfp4_heads* k, int64_t token
 /*
  * mxfp4_qk_norm_rope_bwd -- gradients of mxfp4_qk_norm_rope. dq, dk: gradients
  * of its outputs; q, k: its inputs; rstd: as it wrote it (NULL: there was no norm,
- * or there are no heads).
- * With dz = dy turned back and g = dz weight: dx = r (g - u mean(g u)) to dq_out and dk_out (dense, in `dtype`; without a
- * norm dx = dz, and q and k are not read); dq_weight = sum over tokens and heads
- * of dz u, dk_weight likewise, in weight_dtype (NULL: not wanted; both of them
- * NULL without a norm; zeros where there are no tokens or no heads). Sums in fp32, in a
+ * or there are no heads). With dz = dy turned back and g = dz weight: dx = r (g - u
+ * mean(g u)) to dq_out and dk_out (dense, in `dtype`; without a norm dx = dz, and q
+ * and k are not read: their p may be NULL); dq_weight = sum over tokens and heads of
+ * dz u, dk_weight likewise, in weight_dtype (NULL: not wanted; both of them NULL
+ * without a norm; zeros where there are no tokens or no heads). Sums in fp32, in a
  * fixed order. ws: mxfp4_qk_norm_rope_bwd_workspace_bytes bytes, 4-byte aligned
  * (NULL where both weights' gradients are).
  */

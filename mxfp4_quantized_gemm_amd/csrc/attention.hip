@@ -19,15 +19,16 @@
 // output in the workspace, and a second kernel joins them. The lengths stay on the
 // GPU: a captured graph serves them as they grow.
 //
-// A wave takes 32 tokens at a time, without LDS: the codes go from memory to
-// registers in the layout in which the matrix instructions (16x16x32, f16, fp32
-// sums) take them. Scores: rows are tokens, columns query heads; a lane
-// then has one head's scores of 4 tokens (twice), which is the layout that the
-// second product takes its probabilities in, if its k runs over the tokens in
-// the order (lane / 16) 4 + r of the first 16 and then of the last. Its rows
-// are the head's columns: a lane holds the values of 8 tokens in dim / 16
-// columns, so that bytes become f16 pairs of two tokens without a move between
-// lanes. Outputs have one head a lane, as the scores have.
+// A wave takes 32 tokens at a time. Matrix instructions are 16x16x32, f16, with fp32
+// sums. Scores: rows are tokens, columns query heads; the keys' codes and both scales
+// reach the instructions' layout through a part of the LDS that is the wave's own (see
+// kPitch). A lane then has one head's scores of 4 tokens (twice), which is the layout
+// that the second product takes its probabilities in, if its k runs over the tokens in
+// the order (lane / 16) 4 + r of the first 16 and then of the last. Its rows are the
+// head's columns: the values' codes go from memory to registers in its layout, without
+// LDS, a lane holding those of 8 tokens in dim / 16 columns, so that bytes become f16
+// pairs of two tokens without a move between lanes. Outputs have one head a lane, as
+// the scores have.
 //
 // Codes to f16, two at a time: with the sign flipped a code c is the byte c + 128;
 // a permutation puts two of them into the low bytes of f16 words, where they are
@@ -41,9 +42,9 @@
 // of each, or 2^-39 of the largest). p vs is scaled by a power of two for the
 // largest vs so far, to below 2^14, and enters as the sum of two (2^-24). One is enough
 // for bf16 outputs themselves (2^-12, and calls take up to 4 % less: 64 x 8192 tokens of
-// 32 over 8 heads of 128 175.7 us, not 178.2; the times below are with one), but the 8-bit
-// product behind them rounds again: its result was twice as far from 64 bits as with
-// fp32 probabilities. All sums, the maximum and p are in fp32.
+// 32 over 8 heads of 128 175.7 us, not 178.2), but the 8-bit product behind them rounds
+// again: its result was twice as far from 64 bits as with fp32 probabilities. All sums,
+// the maximum and p are in fp32.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -60,7 +61,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kWaves = kUnitWaves, kThreads = 64 * kWaves;
 constexpr int kGroup = 16;       // query heads of a line
 constexpr int kBatch = 1024;     // sequences of a launch
-constexpr int kMaxGroups = 512;  // work-groups: two on each of the 256 CUs
+// Work-groups that share the units evenly: two on each of the 256 CUs at once, of heads
+// of more than 128 columns one (their registers leave a SIMD one wave, or two).
+constexpr int kMaxGroups = 512;
 constexpr float kNone = -__builtin_inff();
 
 struct Args {
@@ -162,7 +165,9 @@ struct Raw {
   bool ok[2];              // whether the 16 tokens' page is in the cache
 };
 
-// The cache is read once: past the caches (64 x 8000 tokens: 169 us; 189 through them).
+// The cache is read once: past the caches (64 x 8000 tokens, with one number for p vs:
+// 169 us; 189 through them; with two 172 now). Not so the values of heads of 129 to 192
+// columns, whose three words a lane are one ordinary load.
 template <class X>
 __device__ __forceinline__ X load_once(const void* p) {
   return __builtin_nontemporal_load(static_cast<const X*>(p));
@@ -287,9 +292,9 @@ __device__ __forceinline__ float max_groups(float v) {
 
 // K's codes pass through LDS, a wave's tile through 2 to 9 KiB of its own: the
 // matrix instruction's lanes hold 16 tokens side by side, whose rows, loaded so,
-// are 16 cache lines for every 16 lanes (64 x 8000 tokens: 174 us); loaded row after
-// row a 16th of that (169). Rows have 16 bytes more there, so that 16 tokens' reads
-// meet in no bank.
+// are 16 cache lines for every 16 lanes; loaded row after row a 16th of that (64 x 8000
+// tokens, with one number for p vs: 174 us and 169). Rows have 16 bytes more there, so
+// that 16 tokens' reads meet in no bank.
 template <int DP>
 constexpr int kPitch = DP + 16;
 
@@ -770,13 +775,20 @@ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // How a launch is cut: 160 lines or more are left whole, and those of at most two
 // steps of a work-group's waves; others go into about 512 parts. Where work-groups would
-// have more than kChunk tokens, the units are shared evenly. A table's room is what
-// the host knows: parts of short sequences are without work, but none waits for a look
-// at all lengths. (32 query and 8 key heads of 128, bf16, in a graph. 16 sequences of
-// up to 2048 tokens: all of them full 18.8 us, spread evenly from 1 on 15.9, one full
-// and the others of 100 tokens 11.6; in 256 parts 18.6, 15.7, 14.4; shared evenly 20.4,
-// 19.6, 9.9. Whole | in parts: 20 x 1000 tokens 13.1 | 16.4, 30 x 4000 42.7 | 49.1, but
-// 16 x 4000 34.2 | 28.8; 1 x 500 7.6 | 8.3, but 1 x 1000 10.7 | 8.4.)
+// have more than kChunk tokens, the units are shared evenly. (32 query and 8 key heads
+// of 128, bf16, in a graph, tables as wide as the longest sequence. 16 sequences of up to
+// 2048 tokens: all of them full 18.0 to 19.2 us, spread evenly from 1 on 16.2, one full
+// and the others of 100 tokens 11.6; in 256 parts 16.9, 15.7, 14.0; shared evenly 22.7,
+// 18.6, 10.1. Whole | in parts: 20 x 1000 tokens 13.4 | 16.0, 30 x 4000 42.4 | 48.5, but
+// 16 x 4000 35.8 | 28.8; 1 x 500 8.2 | 8.8, but 1 x 1000 11.6 | 8.9.)
+//
+// The host knows a table's room, not the lengths, and does not wait for these: the room
+// sets the cut. Parts of short sequences are without work then, and few work-groups have
+// it all where the tables have room for far more than the sequences hold: one sequence of
+// 1000 tokens takes 8.8 us by its own table, 20.3 by one of 131072 tokens; 4096 tokens 9.3
+// and 35.5; two of 4096 9.5 and 58.2; four (shared evenly then) 12.7 and 14.9. So do one
+// long line among many short ones that are left whole: 24 sequences, one of 4096 tokens
+// and the others of 100, 32 us; all of 4096 tokens 37.9 (shared evenly 12.5 and 43.5).
 struct Cut {
   int64_t splits, chunk;  // splits 0: shared evenly
   int64_t groups;
