@@ -484,8 +484,8 @@ typedef struct {
 /*
  * mxfp4_qk_norm_rope -- for every head x of q and of k: u = x / sqrt(mean(x^2)
  * + eps), z = u weight, and z turned by `rotation` (NULL: not), in fp32 (the mean
- * in fp64, as mxfp4_rmsnorm; its factor in fp32, which a head of a root mean square
- * below 2^-128 and no eps leaves), rounded to `dtype` once. eps < 0: no norm, then
+ * in fp64, as mxfp4_rmsnorm; the factor of x is an fp32 number, infinite where eps is 0
+ * and the root mean square below 2^-128), rounded to `dtype` once. eps < 0: no norm, then
  * the weights are NULL. q_weight, k_weight [dim] of weight_dtype (`dtype` or
  * fp32), NULL for 1. q_out [tokens][q heads][dim], k_out likewise. Either may
  * have no heads. rstd [tokens][q heads + k heads] (NULL: not wanted; not written

@@ -8,7 +8,8 @@ The lengths and page tables stay on the GPU, so a captured graph serves sequence
 as they grow. The work is cut by the tables' width, which the host knows: one or two
 sequences take two to six times as long by a table for 131072 tokens as by one of their
 own length up to 8192, and graphs for a few widths serve them better than one.
-Inference only: inputs that require a gradient are refused. Marshalling only: every step runs in the library's kernels.
+Inference only: inputs that require a gradient are refused.
+Marshalling only: every step runs in the library's kernels.
 """
 from __future__ import annotations
 
